@@ -16,6 +16,9 @@ Functions mirror the C entry points:
 * ``spec_verify_tentative_round`` / ``spec_verify_tentative_flush`` -- the
   hierarchy across calls: intermediate rounds append to a pending state
   (``make_pending``), a flush verifies it against the final exit;
+* ``kv_blocktable_extend``, ``kv_cache_append``, ``kv_paged_attention`` -- the
+  paged cache before a verification: blocks and slots for the new tokens, their
+  keys and values, their attention (``include/spec_kv.h``, ``kv.py``);
 * ``workspace_bytes``, ``validate``, ``device_status``, ``abi_version``.
 """
 
@@ -23,6 +26,10 @@ import ctypes
 import os
 
 import torch
+
+from . import kv as _kv
+from .kv import (KV_EXPORTED, MAX_HEAD_DIM, SV_DTYPE_F16, kv_blocktable_extend,  # noqa: F401
+                 kv_cache_append, kv_paged_attention, kv_paged_attention_workspace_bytes)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # SPEC_VERIFY_LIB names another build of the same library (the host-sanitizer
@@ -149,6 +156,7 @@ def load_library(path):
     lib.spec_verify_tentative_flush.restype = i32
     lib.spec_verify_tentative_flush.argtypes = [ctypes.POINTER(Desc), P, P, i32,
                                                 ctypes.POINTER(Pending), P, P, P, P, P, sz, P]
+    _kv.set_signatures(lib)
     return lib
 
 

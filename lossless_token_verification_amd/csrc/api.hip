@@ -874,6 +874,18 @@ int32_t scratch_address(hipStream_t st, void** out) {
 
 }  // namespace
 
+namespace sv {
+// The other C entry points' failures (kvapi.hip) share the thread's message.
+int32_t record_error(int32_t code, const char* msg) noexcept {
+  try {
+    g_last_error = msg;
+  } catch (...) {
+    g_last_error.clear();   // no memory for the text: the status still stands
+  }
+  return code;
+}
+}  // namespace sv
+
 extern "C" {
 
 int32_t spec_verify_abi_version(void) { return SPEC_VERIFY_ABI_VERSION; }

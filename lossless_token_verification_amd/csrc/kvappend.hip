@@ -1,0 +1,45 @@
+// Cache append: each token's key and value rows go to their slot, head by
+// head ([blocks, kv_heads, block_size, head_dim]).  A copy: one vector of k
+// and one of v per thread, both loads before both stores.
+#include "kv_args.h"
+
+namespace sv {
+
+namespace {
+
+constexpr int kAppendThreads = 256;
+
+template <typename V>
+__global__ __launch_bounds__(kAppendThreads) void append_kernel(AppendArgs a, int64_t total) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kAppendThreads + threadIdx.x;
+  if (i >= total) return;
+  const int t = static_cast<int>(i / a.row_vecs);
+  const int c = static_cast<int>(i - static_cast<int64_t>(t) * a.row_vecs);
+  const int64_t slot = a.slots[t];
+  if (slot < 0 || slot >= a.num_slots) return;
+  const int h = fast_div(c, a.head), d = c - h * a.head_vecs;
+  const int blk = fast_div(static_cast<int>(slot), a.bs);
+  const int row = static_cast<int>(slot) - blk * a.block_size;
+  const int64_t at = blk * a.block_stride +
+                     (static_cast<int64_t>(h) * a.block_size + row) * a.head_vecs + d;
+  const V kv = static_cast<const V*>(a.src[0])[t * a.src_stride[0] + c];
+  const V vv = static_cast<const V*>(a.src[1])[t * a.src_stride[1] + c];
+  static_cast<V*>(a.dst[0])[at] = kv;
+  static_cast<V*>(a.dst[1])[at] = vv;
+}
+
+}  // namespace
+
+hipError_t launch_append(const AppendArgs& a, hipStream_t st) {
+  const int64_t total = static_cast<int64_t>(a.T) * a.row_vecs;
+  const dim3 grid(static_cast<unsigned>((total + kAppendThreads - 1) / kAppendThreads));
+  if (a.vec_bytes == 16)
+    hipLaunchKernelGGL(append_kernel<u32x4>, grid, dim3(kAppendThreads), 0, st, a, total);
+  else if (a.vec_bytes == 4)
+    hipLaunchKernelGGL(append_kernel<uint32_t>, grid, dim3(kAppendThreads), 0, st, a, total);
+  else
+    hipLaunchKernelGGL(append_kernel<uint16_t>, grid, dim3(kAppendThreads), 0, st, a, total);
+  return hipGetLastError();
+}
+
+}  // namespace sv

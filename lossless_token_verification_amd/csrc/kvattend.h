@@ -1,0 +1,190 @@
+// Device code shared by the paged-attention kernels: which (tile, split) of
+// which sequence a workgroup takes, and the form of a split's partial result.
+#pragma once
+
+#include "kv_args.h"
+
+namespace sv {
+
+// One workgroup's share: query rows [row0, row0 + rows) of a sequence and the
+// key units [u0, u1) of its split.
+struct AttendItem {
+  int32_t token0, row0, rows;
+  int32_t pos0;              // position of the sequence's first new token
+  int32_t b;
+  int32_t key_lo, key_hi;    // positions any row of the tile may see
+  int32_t u0, u1;
+  int32_t split, splits, slot;   // slot: partial slot (splits > 1)
+};
+
+struct AttendSeq {
+  int64_t pos0;
+  int32_t token0, n, tiles, units, kmax;
+};
+
+// A sequence's extent; every value read from the device arrays is limited to
+// what the descriptor allows, so that nothing out of range is ever addressed.
+template <int MT, int KT>
+__device__ __forceinline__ AttendSeq attend_seq(const AttendArgs& a, int b) {
+  AttendSeq s;
+  const int c0 = min(max(a.cu[b], 0), a.T), c1 = min(max(a.cu[b + 1], c0), a.T);
+  const int L = max(a.lens[b], 0);
+  s.token0 = c0;
+  s.n = c1 - c0;
+  s.pos0 = static_cast<int64_t>(L) - s.n;
+  s.kmax = min(L, a.cap);
+  s.tiles = static_cast<int>((static_cast<int64_t>(s.n) * a.group + MT - 1) / MT);
+  const int64_t lo = a.window > 0 ? max(s.pos0 - a.window + 1, static_cast<int64_t>(0)) : 0;
+  s.units = s.kmax > lo ? static_cast<int>((s.kmax + static_cast<int64_t>(KT) - 1) / KT - lo / KT)
+                        : 0;
+  return s;
+}
+
+// Inclusive prefix sum over a wavefront.
+__device__ __forceinline__ uint64_t wave_prefix(uint64_t v) {
+  const int lane = threadIdx.x & (kWave - 1);
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) {
+    const uint64_t u = __shfl_up(static_cast<unsigned long long>(v), o, kWave);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+
+template <int WAVES>
+struct AttendPlanShared {
+  uint64_t sum[2][WAVES];
+  AttendItem item;
+  int32_t found;
+};
+
+// Finds item x of the call.  All threads of the workgroup call it; false (for
+// all of them) if there are fewer items.
+//
+// A sequence's keys are cut into splits of about S units, where S is what
+// spreads the call's units evenly over want_items workgroups and at least
+// min_units: with many tiles nothing is split, with few rows the key axis
+// fills the chip.  sum tiles * ceil(units / S) <= want_items + tiles, which
+// bounds the launch; the sequences that are split have units > S, so they use
+// at most 2 * want_items partial slots.  Every workgroup makes these sums
+// itself (two prefix passes over the batch, from cache), which costs less than
+// the launch that a separate planning kernel would be.
+template <int MT, int KT, int WAVES>
+__device__ __forceinline__ bool attend_find(const AttendArgs& a, int x, bool count_slots,
+                                            AttendPlanShared<WAVES>& sh, AttendItem& it) {
+  constexpr int NT = WAVES * kWave;
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  int64_t S = INT32_MAX;
+  if (a.max_slots > 0) {
+    uint64_t units = 0;
+    for (int b = tid; b < a.B; b += NT) {
+      const AttendSeq s = attend_seq<MT, KT>(a, b);
+      units += static_cast<uint64_t>(s.tiles) * s.units;
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1)
+      units += __shfl_xor(static_cast<unsigned long long>(units), o, kWave);
+    if (WAVES > 1) {
+      if (lane == 0) sh.sum[0][wave] = units;
+      __syncthreads();
+      units = 0;
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) units += sh.sum[0][w];
+    }
+    S = max(static_cast<int64_t>(a.min_units),
+            static_cast<int64_t>((units + a.want_items - 1) / a.want_items));
+  }
+  if (tid == 0) sh.found = 0;
+  uint64_t carry = 0;   // (items << 32) + slots of the sequences before this chunk
+  for (int c = 0; c < a.B; c += NT) {
+    const int b = c + tid;
+    AttendSeq s{};
+    int splits = 1;
+    uint64_t mine = 0;
+    if (b < a.B) {
+      s = attend_seq<MT, KT>(a, b);
+      if (s.units > S) splits = static_cast<int>((s.units + S - 1) / S);
+      const uint64_t items = static_cast<uint64_t>(s.tiles) * splits;
+      mine = (items << 32) + (splits > 1 ? items : 0);
+    }
+    uint64_t v = wave_prefix(mine);
+    uint64_t all = 0, before = carry;
+    if (WAVES > 1) {
+      __syncthreads();
+      if (lane == kWave - 1) sh.sum[1][wave] = v;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) {
+        if (w < wave) before += sh.sum[1][w];
+        all += sh.sum[1][w];
+      }
+    } else {
+      all = __shfl(static_cast<unsigned long long>(v), kWave - 1, kWave);
+    }
+    before += v - mine;
+    carry += all;
+    const int64_t y = x - static_cast<int64_t>(before >> 32);
+    if (y >= 0 && y < static_cast<int64_t>(mine >> 32)) {
+      // the tiles of a sequence from its last (with the most keys) to its first
+      const int split = static_cast<int>(y % splits);
+      const int tile = s.tiles - 1 - static_cast<int>(y / splits);
+      const int rows_all = s.n * a.group;
+      AttendItem r;
+      r.b = b;
+      r.token0 = s.token0;
+      r.row0 = tile * MT;
+      r.rows = min(MT, rows_all - r.row0);
+      r.pos0 = static_cast<int32_t>(s.pos0);
+      const int j0 = fast_div(r.row0, a.grp), j1 = fast_div(r.row0 + r.rows - 1, a.grp);
+      const int64_t hi = min(s.pos0 + j1 + 1, static_cast<int64_t>(s.kmax));
+      const int64_t lo = a.window > 0 ? max(s.pos0 + j0 - a.window + 1, static_cast<int64_t>(0)) : 0;
+      r.key_lo = static_cast<int32_t>(min(lo, max(hi, static_cast<int64_t>(0))));
+      r.key_hi = static_cast<int32_t>(max(hi, static_cast<int64_t>(r.key_lo)));
+      const int f = r.key_lo / KT;
+      const int e = r.key_hi > r.key_lo ? (r.key_hi - 1) / KT + 1 : f;
+      const int len = (e - f + splits - 1) / splits;
+      r.u0 = min(e, f + split * len);
+      r.u1 = min(e, r.u0 + len);
+      r.split = split;
+      r.splits = splits;
+      r.slot = static_cast<int32_t>(static_cast<uint32_t>(before)) + tile * splits + split;
+      sh.item = r;
+      sh.found = 1;
+    }
+    if (static_cast<int64_t>(carry >> 32) > x && !count_slots) break;
+  }
+  if (count_slots && tid == 0)
+    *a.slot_count = static_cast<int32_t>(min(static_cast<uint32_t>(carry),
+                                             static_cast<uint32_t>(a.max_slots)));
+  __syncthreads();
+  if (!sh.found) return false;
+  it = sh.item;
+  return it.splits == 1 || it.slot < a.max_slots;
+}
+
+// What a split leaves for the joining launch: the unnormalised output of each
+// row relative to its maximum (in log2 units, -inf where it saw nothing) and
+// the sum of its weights.
+__device__ __forceinline__ void attend_slot_info(const AttendArgs& a, const AttendItem& it) {
+  SlotInfo s{};
+  s.split = it.split;
+  s.splits = it.splits;
+  s.token0 = it.token0;
+  s.row0 = it.row0;
+  s.rows = it.rows;
+  a.info[it.slot] = s;
+}
+
+// Row r of a tile: token row and query head.
+__device__ __forceinline__ void attend_row(const AttendArgs& a, int token0, int row, int h,
+                                           int& token, int& head) {
+  const int j = fast_div(row, a.grp);
+  token = token0 + j;
+  head = h * a.group + (row - j * a.group);
+}
+
+AttendShape attend_shape(int dtype, int D);
+hipError_t launch_attend_rows(const AttendArgs& a, int dtype, hipStream_t st);
+hipError_t launch_attend_join(const AttendArgs& a, int dtype, int mt, hipStream_t st);
+
+}  // namespace sv

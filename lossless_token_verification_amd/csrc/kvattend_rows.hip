@@ -1,0 +1,298 @@
+// Paged attention on the vector units (float32 caches, and head sizes without
+// a matrix-core kernel), and the launch that joins splits.
+//
+// One workgroup takes a few query rows and a split of their keys; its
+// wavefronts take 8 keys a step each, 8 lanes to a key, so that a key's row is
+// read in whole 128-byte lines and a dot product needs three exchanges.
+// Softmax in one pass: every group of 8 lanes keeps its own running maximum m
+// and sum l and the output relative to it; a new maximum scales both by
+// 2^(m_old - m_new).  The groups' states are merged once at the end.
+#include "kvattend.h"
+
+namespace sv {
+
+namespace {
+
+typedef _Float16 half_t;
+
+template <typename T>
+struct Elem;
+template <>
+struct Elem<float> {
+  static constexpr int kPerVec = 4;
+  __device__ static void load(const u32x4& w, float* f) {
+    f[0] = __uint_as_float(w.x);
+    f[1] = __uint_as_float(w.y);
+    f[2] = __uint_as_float(w.z);
+    f[3] = __uint_as_float(w.w);
+  }
+  __device__ static float store(float x) { return x; }
+};
+template <>
+struct Elem<__bf16> {
+  static constexpr int kPerVec = 8;
+  __device__ static void load(const u32x4& w, float* f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = bf16_lo(w[i]);
+      f[2 * i + 1] = bf16_hi(w[i]);
+    }
+  }
+  __device__ static __bf16 store(float x) { return static_cast<__bf16>(x); }
+};
+template <>
+struct Elem<half_t> {
+  static constexpr int kPerVec = 8;
+  __device__ static void load(const u32x4& w, float* f) {
+    typedef half_t h8 __attribute__((ext_vector_type(8)));
+    const h8 x = __builtin_bit_cast(h8, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = static_cast<float>(x[i]);
+  }
+  __device__ static half_t store(float x) { return static_cast<half_t>(x); }
+};
+
+constexpr int kRowWaves = 4;
+constexpr int kKeysPerStep = 8;
+constexpr int kRowKT = kRowsKT;
+static_assert(kRowWaves * kKeysPerStep == kRowKT, "keys per unit");
+
+// NF: floats of a row each of the 8 lanes of a key holds (8 * NF >= head_dim).
+template <typename T, int NF, int R>
+__global__ __launch_bounds__(kRowWaves * kWave) void attend_rows_kernel(AttendArgs a) {
+  constexpr int PV = Elem<T>::kPerVec, NV = NF / PV;
+  __shared__ AttendPlanShared<kRowWaves> plan;
+  __shared__ float so[kRowWaves][R][8 * NF];
+  __shared__ float sm[kRowWaves][R], sl[kRowWaves][R];
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  const int x = blockIdx.x / a.kv_heads, h = blockIdx.x - x * a.kv_heads;
+  AttendItem it;
+  if (!attend_find<R, kRowKT, kRowWaves>(a, x, a.max_slots > 0 && blockIdx.x == 0, plan, it))
+    return;
+  if (it.splits > 1 && h == 0 && tid == 0) attend_slot_info(a, it);
+
+  const int sub = lane & 7, kg = lane >> 3;
+  const int nv = a.D / PV;
+  const float c = a.scale * kLog2e;
+  float q[R][NF], o[R][NF], m[R], l[R];
+  int pos[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    int token, head;
+    attend_row(a, it.token0, it.row0 + min(r, it.rows - 1), h, token, head);
+    pos[r] = it.pos0 + token - it.token0;
+    const T* qr = static_cast<const T*>(a.q) + token * a.q_stride + static_cast<int64_t>(head) * a.D;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = sub + 8 * i;
+      u32x4 w = {0, 0, 0, 0};
+      if (v < nv) w = reinterpret_cast<const u32x4*>(qr)[v];
+      Elem<T>::load(w, &q[r][i * PV]);
+    }
+    m[r] = -INFINITY;
+    l[r] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NF; ++i) o[r][i] = 0.0f;
+  }
+
+  const int32_t* table = a.table + static_cast<int64_t>(it.b) * a.max_blocks;
+  const int64_t head_off = static_cast<int64_t>(h) * a.block_size;
+  for (int u = it.u0; u < it.u1; ++u) {
+    const int key = u * kRowKT + wave * kKeysPerStep + kg;
+    bool in = key >= it.key_lo && key < it.key_hi;
+    int64_t off = 0;
+    if (in) {
+      const int lb = fast_div(key, a.bs);
+      const int id = table[lb];
+      in = id >= 0 && id < a.num_blocks;
+      off = id * a.block_stride + (head_off + (key - lb * a.block_size)) * a.D;
+    }
+    u32x4 kw[NV], vw[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = sub + 8 * i;
+      kw[i] = vw[i] = u32x4{0, 0, 0, 0};
+      if (in && v < nv) {
+        kw[i] = reinterpret_cast<const u32x4*>(static_cast<const T*>(a.k) + off)[v];
+        vw[i] = reinterpret_cast<const u32x4*>(static_cast<const T*>(a.v) + off)[v];
+      }
+    }
+    float s[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) s[r] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float kf[PV];
+      Elem<T>::load(kw[i], kf);
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int e = 0; e < PV; ++e) s[r] = fmaf(q[r][i * PV + e], kf[e], s[r]);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      s[r] += __shfl_xor(s[r], 1, kWave);
+      s[r] += __shfl_xor(s[r], 2, kWave);
+      s[r] += __shfl_xor(s[r], 4, kWave);
+    }
+    float vf[NF];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) Elem<T>::load(vw[i], &vf[i * PV]);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      // a position the row does not see leaves its state alone, whatever it holds
+      if (!in || key > pos[r] ||
+          (a.window > 0 && static_cast<int64_t>(key) <= static_cast<int64_t>(pos[r]) - a.window))
+        continue;
+      const float t = s[r] * c;
+      const float mn = fmaxf(m[r], t), ref = mn == -INFINITY ? 0.0f : mn;
+      const float f = __builtin_amdgcn_exp2f(m[r] - ref), p = __builtin_amdgcn_exp2f(t - ref);
+      m[r] = mn;
+      l[r] = fmaf(l[r], f, p);
+#pragma unroll
+      for (int i = 0; i < NF; ++i) o[r][i] = fmaf(p, vf[i], o[r][i] * f);
+    }
+  }
+
+  // merge the wavefront's 8 key groups, then the wavefronts
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    float mw = m[r];
+#pragma unroll
+    for (int b = 8; b < kWave; b <<= 1) mw = fmaxf(mw, __shfl_xor(mw, b, kWave));
+    const float f = __builtin_amdgcn_exp2f(m[r] - (mw == -INFINITY ? 0.0f : mw));
+    l[r] *= f;
+#pragma unroll
+    for (int b = 8; b < kWave; b <<= 1) l[r] += __shfl_xor(l[r], b, kWave);
+#pragma unroll
+    for (int i = 0; i < NF; ++i) {
+      float t = o[r][i] * f;
+#pragma unroll
+      for (int b = 8; b < kWave; b <<= 1) t += __shfl_xor(t, b, kWave);
+      if (kg == 0) so[wave][r][(sub + 8 * (i / PV)) * PV + i % PV] = t;
+    }
+    if (lane == 0) {
+      sm[wave][r] = mw;
+      sl[wave][r] = l[r];
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < R * a.D; i += kRowWaves * kWave) {
+    const int r = i / a.D, d = i - r * a.D;
+    if (r >= it.rows) break;
+    float mw = sm[0][r];
+#pragma unroll
+    for (int w = 1; w < kRowWaves; ++w) mw = fmaxf(mw, sm[w][r]);
+    const float ref = mw == -INFINITY ? 0.0f : mw;
+    float lw = 0.0f, ow = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kRowWaves; ++w) {
+      const float f = __builtin_amdgcn_exp2f(sm[w][r] - ref);
+      lw = fmaf(sl[w][r], f, lw);
+      ow = fmaf(so[w][r][d], f, ow);
+    }
+    if (it.splits > 1) {
+      const int64_t p = (static_cast<int64_t>(it.slot) * a.kv_heads + h) * R + r;
+      a.part_o[p * a.D + d] = ow;
+      if (d == 0) {
+        a.part_ml[p * 2] = mw;
+        a.part_ml[p * 2 + 1] = lw;
+      }
+    } else {
+      int token, head;
+      attend_row(a, it.token0, it.row0 + r, h, token, head);
+      const int64_t at = static_cast<int64_t>(token) * a.heads + head;
+      static_cast<T*>(a.out)[at * a.D + d] = Elem<T>::store(lw == 0.0f ? 0.0f : ow / lw);
+      if (a.lse && d == 0) a.lse[at] = lw == 0.0f ? -INFINITY : (mw + log2f(lw)) * kLn2;
+    }
+  }
+}
+
+// Joins the splits of the tiles that were split: out = sum_s 2^(m_s - M) O_s /
+// sum_s 2^(m_s - M) l_s.  One workgroup per slot and key head; the slots of a
+// tile share its rows, and the wavefronts share a row's splits, which are
+// added in a fixed order.
+template <typename T>
+__global__ __launch_bounds__(kRowWaves * kWave) void attend_join_kernel(AttendArgs a, int mt) {
+  __shared__ float so[kRowWaves][kMaxHeadDim];
+  __shared__ float sl[kRowWaves], sm[kRowWaves];
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  const int slot = blockIdx.x / a.kv_heads, h = blockIdx.x - slot * a.kv_heads;
+  const SlotInfo s = a.info[slot];
+  if (slot >= *a.slot_count) return;
+  const int first = slot - s.split;
+  const int64_t step = static_cast<int64_t>(a.kv_heads) * mt;
+  for (int r = s.split; r < s.rows; r += s.splits) {
+    const int64_t p0 = (static_cast<int64_t>(first) * a.kv_heads + h) * mt + r;
+    float mx = -INFINITY;
+    for (int i = tid; i < s.splits; i += kRowWaves * kWave)
+      mx = fmaxf(mx, a.part_ml[(p0 + i * step) * 2]);
+    mx = wave_max(mx);
+    __syncthreads();   // sm, sl and so of the row before are read
+    if (lane == 0) sm[wave] = mx;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kRowWaves; ++w) mx = fmaxf(mx, sm[w]);
+    const float ref = mx == -INFINITY ? 0.0f : mx;
+    float o[4] = {0.0f, 0.0f, 0.0f, 0.0f}, l = 0.0f;
+#pragma unroll 4
+    for (int i = wave; i < s.splits; i += kRowWaves) {
+      const int64_t p = p0 + i * step;
+      const float f = __builtin_amdgcn_exp2f(a.part_ml[p * 2] - ref);
+      l = fmaf(a.part_ml[p * 2 + 1], f, l);
+      const float* po = a.part_o + p * a.D;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (lane + j * kWave < a.D) o[j] = fmaf(po[lane + j * kWave], f, o[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (lane + j * kWave < a.D) so[wave][lane + j * kWave] = o[j];
+    if (lane == 0) sl[wave] = l;
+    __syncthreads();
+    float lw = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kRowWaves; ++w) lw += sl[w];
+    int token, head;
+    attend_row(a, s.token0, s.row0 + r, h, token, head);
+    const int64_t at = static_cast<int64_t>(token) * a.heads + head;
+    if (tid < a.D) {
+      float ow = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kRowWaves; ++w) ow += so[w][tid];
+      static_cast<T*>(a.out)[at * a.D + tid] = Elem<T>::store(lw == 0.0f ? 0.0f : ow / lw);
+    }
+    if (a.lse && tid == 0) a.lse[at] = lw == 0.0f ? -INFINITY : (ref + log2f(lw)) * kLn2;
+  }
+}
+
+template <typename T>
+void rows_of(const AttendArgs& a, dim3 grid, hipStream_t st) {
+  const dim3 block(kRowWaves * kWave);
+  if (a.D <= 64)
+    hipLaunchKernelGGL((attend_rows_kernel<T, 8, kRowsMT64>), grid, block, 0, st, a);
+  else if (a.D <= 128)
+    hipLaunchKernelGGL((attend_rows_kernel<T, 16, kRowsMT128>), grid, block, 0, st, a);
+  else
+    hipLaunchKernelGGL((attend_rows_kernel<T, 32, kRowsMT256>), grid, block, 0, st, a);
+}
+
+}  // namespace
+
+hipError_t launch_attend_rows(const AttendArgs& a, int dtype, hipStream_t st) {
+  const dim3 grid(static_cast<unsigned>(a.grid_items) * a.kv_heads);
+  if (dtype == kF32) rows_of<float>(a, grid, st);
+  else if (dtype == kBF16) rows_of<__bf16>(a, grid, st);
+  else rows_of<half_t>(a, grid, st);
+  return hipGetLastError();
+}
+
+hipError_t launch_attend_join(const AttendArgs& a, int dtype, int mt, hipStream_t st) {
+  const dim3 grid(static_cast<unsigned>(a.max_slots) * a.kv_heads), block(kRowWaves * kWave);
+  if (dtype == kF32) hipLaunchKernelGGL(attend_join_kernel<float>, grid, block, 0, st, a, mt);
+  else if (dtype == kBF16) hipLaunchKernelGGL(attend_join_kernel<__bf16>, grid, block, 0, st, a, mt);
+  else hipLaunchKernelGGL(attend_join_kernel<half_t>, grid, block, 0, st, a, mt);
+  return hipGetLastError();
+}
+
+}  // namespace sv

@@ -1,0 +1,198 @@
+// Block-table extension: prefix sums over the sequences give every sequence
+// its rows in the packed token arrays and its place in the pool's stack; each
+// token's slot then follows from its position alone.
+//
+// With L_b tokens held and n_b new ones (page size s):
+//   need_b = ceil((L_b + n_b) / s) - ceil(L_b / s),  off_b = sum_{b' < b} need_b',
+//   block i of b = stack[top - 1 - off_b - i],  cu_b = sum_{b' < b} n_b'.
+// A new logical block starts at a position >= L_b, which is always a new
+// token's, so the token standing there writes the block's table entry, and
+// every token computes its slot from the stack without waiting for a table
+// write.
+//
+// The bytes are few (12 per token, a handful per sequence), so what counts is
+// the latency of the launches: one workgroup makes the prefix sums and, up to
+// kFusedTokens tokens, fills the token arrays itself; beyond that a second
+// launch spreads the fill over the chip.
+#include "kv_args.h"
+
+namespace sv {
+
+namespace {
+
+constexpr int kScanThreads = 1024;     // most threads of the prefix-sum workgroup
+constexpr int kFillThreads = 256;
+constexpr int kFillTokens = 1024;      // tokens per workgroup of the fill launch
+constexpr int kFusedTokens = 8192;
+
+// Exclusive prefix sum over the workgroup's threads; *total gets the sum.
+// scratch: one value per wavefront.
+__device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* scratch, int64_t* total) {
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  const int waves = blockDim.x / kWave;
+  int64_t v = x;
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) {
+    const int64_t u = __shfl_up(static_cast<long long>(v), o, kWave);
+    if (lane >= o) v += u;
+  }
+  __syncthreads();   // scratch may still be read from the scan before
+  if (lane == kWave - 1) scratch[wave] = v;
+  __syncthreads();
+  int64_t before = 0, all = 0;
+  for (int w = 0; w < waves; ++w) {
+    if (w < wave) before += scratch[w];
+    all += scratch[w];
+  }
+  *total = all;
+  return before + v - x;
+}
+
+__device__ __forceinline__ int64_t ceil_blocks(int64_t n, const FastDiv& bs) {
+  // n <= 2^31 - 1: the quotient of n - 1 never leaves the exact range
+  return n > 0 ? fast_div(static_cast<int>(n - 1), bs) + 1 : 0;
+}
+
+// Fills rows [t0, t1) of the token arrays from the plan's outputs (cu,
+// new_lens, num_taken, free_left), a chunk of blockDim.x sequences at a time.
+__device__ void fill_tokens(const ExtendArgs& a, int t0, int t1, int64_t* scratch, int32_t* s_cu,
+                            int32_t* s_len, int64_t* s_off) {
+  const int tid = threadIdx.x, nt = blockDim.x;
+  const int used = a.cu[a.B];
+  for (int t = max(t0, used) + tid; t < t1; t += nt) {
+    a.slots[t] = -1;
+    if (a.positions) a.positions[t] = -1;
+  }
+  // ids in the stack before any was taken: what is left and what was taken
+  int64_t taken_all = 0;
+  if (a.B > nt)
+    for (int c = 0; c < a.B; c += nt) {
+      int64_t sum;
+      block_scan(c + tid < a.B ? max(a.num_taken[c + tid], 0) : 0, scratch, &sum);
+      taken_all += sum;
+    }
+  int64_t carry = 0;
+  for (int c = 0; c < a.B; c += nt) {
+    const int b = c + tid, m = min(nt, a.B - c);
+    const int32_t got = b < a.B ? a.num_taken[b] : 0;
+    int64_t sum;
+    const int64_t off = carry + block_scan(max(got, 0), scratch, &sum);
+    if (a.B <= nt) taken_all = sum;
+    carry += sum;
+    const int64_t top = a.free_left[0] + taken_all;
+    if (b < a.B) {
+      const int32_t lo = a.cu[b];
+      s_cu[tid] = lo;
+      if (b == a.B - 1 || tid == nt - 1) s_cu[tid + 1] = a.cu[b + 1];
+      s_len[tid] = got >= 0 ? a.new_lens[b] - (a.cu[b + 1] - lo) : -1;   // -1: not served
+      s_off[tid] = top - 1 - off;
+    }
+    __syncthreads();
+    const int lo = max(t0, s_cu[0]), hi = min(t1, s_cu[m]);
+    for (int t = lo + tid; t < hi; t += nt) {
+      int l = 0, r = m;   // the last sequence of the chunk that starts at or before t
+      while (r - l > 1) {
+        const int mid = (l + r) >> 1;
+        if (s_cu[mid] <= t) l = mid; else r = mid;
+      }
+      const int len = s_len[l];
+      if (len < 0) {
+        a.slots[t] = -1;
+        if (a.positions) a.positions[t] = -1;
+        continue;
+      }
+      const int pos = len + (t - s_cu[l]);
+      const int lb = fast_div(pos, a.bs), row = pos - lb * a.block_size;
+      const int64_t fresh = lb - ceil_blocks(len, a.bs);   // index among the blocks just taken
+      int32_t* entry = a.table + static_cast<int64_t>(c + l) * a.max_blocks + lb;
+      int32_t id;
+      if (fresh >= 0) {
+        id = a.free_blocks[s_off[l] - fresh];
+        if (row == 0) *entry = id;
+      } else {
+        id = *entry;
+      }
+      a.slots[t] = static_cast<int64_t>(id) * a.block_size + row;
+      if (a.positions) a.positions[t] = pos;
+    }
+    __syncthreads();
+  }
+}
+
+struct FillShared {
+  int64_t scratch[kScanThreads / kWave];
+  int64_t off[kScanThreads];
+  int32_t cu[kScanThreads + 1];
+  int32_t len[kScanThreads];
+};
+
+__global__ __launch_bounds__(kScanThreads) void extend_kernel(ExtendArgs a, int fused) {
+  __shared__ FillShared sh;
+  const int tid = threadIdx.x, nt = blockDim.x;
+  int64_t top = min(max(a.free_count[0], 0), a.free_capacity);
+  if (a.freed) {
+    for (int c = 0; c < a.B; c += nt) {
+      const int b = c + tid;
+      const int m = b < a.B ? min(max(a.num_freed[b], 0), a.max_freed) : 0;
+      int64_t sum;
+      const int64_t at = top + block_scan(m, sh.scratch, &sum);
+      for (int i = 0; i < m && at + i < a.free_capacity; ++i)
+        a.free_blocks[at + i] = a.freed[static_cast<int64_t>(b) * a.max_freed + i];
+      top = min(top + sum, static_cast<int64_t>(a.free_capacity));
+    }
+  }
+  const int64_t cap = min(static_cast<int64_t>(a.max_blocks) * a.block_size,
+                          static_cast<int64_t>(INT32_MAX));
+  int64_t rows = 0, taken = 0;   // tokens and blocks of the chunks before
+  int64_t given = 0;             // blocks handed out
+  for (int c = 0; c < a.B; c += nt) {
+    const int b = c + tid;
+    const int64_t L = b < a.B ? a.lens[b] : 0, n = b < a.B ? a.num_new[b] : 0;
+    const int64_t want = max(n, static_cast<int64_t>(0));
+    int64_t sum;
+    const int64_t first = rows + block_scan(want, sh.scratch, &sum);
+    rows += sum;
+    const bool good = n >= 0 && L >= 0 && L + n <= cap && first + want <= a.T;
+    const int64_t need = good ? ceil_blocks(L + n, a.bs) - ceil_blocks(L, a.bs) : 0;
+    const int64_t off = taken + block_scan(need, sh.scratch, &sum);
+    taken += sum;
+    const bool served = good && (need == 0 || off + need <= top);
+    if (b < a.B) {
+      a.new_lens[b] = static_cast<int32_t>(served ? L + n : L);
+      a.num_taken[b] = served ? static_cast<int32_t>(need) : good ? -2 : -1;
+      a.cu[b] = static_cast<int32_t>(min(first, static_cast<int64_t>(a.T)));
+    }
+    block_scan(served ? need : 0, sh.scratch, &sum);
+    given += sum;
+  }
+  if (tid == 0) {
+    a.cu[a.B] = static_cast<int32_t>(min(rows, static_cast<int64_t>(a.T)));
+    a.free_left[0] = static_cast<int32_t>(top - given);
+  }
+  if (!fused) return;
+  __syncthreads();
+  fill_tokens(a, 0, a.T, sh.scratch, sh.cu, sh.len, sh.off);
+}
+
+__global__ __launch_bounds__(kFillThreads) void fill_kernel(ExtendArgs a) {
+  __shared__ FillShared sh;
+  const int t0 = blockIdx.x * kFillTokens;
+  fill_tokens(a, t0, min(a.T, t0 + kFillTokens), sh.scratch, sh.cu, sh.len, sh.off);
+}
+
+}  // namespace
+
+hipError_t launch_extend(const ExtendArgs& a, hipStream_t st) {
+  const int fused = a.T <= kFusedTokens;
+  const int work = max(a.B, fused ? min(a.T, kScanThreads) : 0);
+  const unsigned threads = static_cast<unsigned>(
+      min(kScanThreads, max(kWave, (work + kWave - 1) / kWave * kWave)));
+  hipLaunchKernelGGL(extend_kernel, dim3(1), dim3(threads), 0, st, a, fused);
+  hipError_t err = hipGetLastError();
+  if (err != hipSuccess || fused) return err;
+  hipLaunchKernelGGL(fill_kernel, dim3((a.T + kFillTokens - 1) / kFillTokens), dim3(kFillThreads),
+                     0, st, a);
+  return hipGetLastError();
+}
+
+}  // namespace sv

@@ -37,6 +37,8 @@ lmhead     logits of a linear LM head (hidden . W^T, float64) fed to the
            single-stage verify.
 byproducts row entropies and the verification-outcome export (acceptance
            probability and largest residual tokens per tested position).
+pagedkv    growing block tables and slot maps, the cache append, attention over
+           the pages (with the magnitudes that its error bounds need).
 tentative  cross-call tentative buffering: intermediate rounds append to a
            per-sequence pending state, a flush verifies it against the final
            exit.
@@ -47,4 +49,4 @@ exposes; their round structure is pinned through the 4x64 instantiation
 against ``numpy.random.Philox`` and the constants are the published ones.
 """
 
-from . import philox, numerics, rule, verify, blocktable, byproducts, tentative  # noqa: F401
+from . import philox, numerics, rule, verify, blocktable, byproducts, pagedkv, tentative  # noqa: F401
