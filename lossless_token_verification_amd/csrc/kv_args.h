@@ -105,6 +105,7 @@ constexpr int kRowsMT64 = 4, kRowsMT128 = 4, kRowsMT256 = 2, kRowsKT = 32;
 // the chip, keys a split is worth at least.
 struct AttendShape {
   int32_t mt, kt, wgs, min_units;
+  bool matrix;   // on the matrix cores
 };
 
 }  // namespace sv

@@ -91,6 +91,30 @@ struct AttendPlan {
 
 size_t pad256(size_t n) { return (n + 255) / 256 * 256; }
 
+// The kernel for a call: the matrix-core one where types and head size have it,
+// with the smallest tile that takes the rows of one sequence and key head
+// (rows: the caller's max_new, or the batch's mean, times the heads of a group).
+sv::AttendShape attend_shape(const spec_kv_attention_desc& d) {
+  sv::AttendShape s{};
+  const int D = d.head_dim;
+  s.matrix = d.dtype != SV_DTYPE_F32 && (D == 64 || D == 128 || D == 256) && d.num_blocks > 0;
+  if (s.matrix) {
+    const int64_t mean = d.batch > 0 ? (static_cast<int64_t>(d.tokens) + d.batch - 1) / d.batch : 1;
+    const int64_t n = std::min<int64_t>(d.max_new > 0 ? d.max_new : mean, d.tokens);
+    const int64_t rows = n * (d.heads / d.kv_heads);
+    s.mt = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+    s.kt = D == 256 ? 32 : 64;
+    s.wgs = 1024;
+    s.min_units = 256 / s.kt;
+  } else {
+    s.mt = D <= 64 ? sv::kRowsMT64 : D <= 128 ? sv::kRowsMT128 : sv::kRowsMT256;
+    s.kt = sv::kRowsKT;
+    s.wgs = 1024;
+    s.min_units = 256 / s.kt;
+  }
+  return s;
+}
+
 int32_t make_attend_plan(const spec_kv_attention_desc* d, AttendPlan* p) {
   if (!d) return fail(SV_ERR_INVALID_ARG, "desc is NULL");
   if (d->reserved != 0 || d->reserved_f != 0.0f)
@@ -120,7 +144,7 @@ int32_t make_attend_plan(const spec_kv_attention_desc* d, AttendPlan* p) {
     return fail(SV_ERR_MISALIGNED, "q_stride and block_stride must be multiples of 16 bytes");
 
   const int64_t group = d->heads / d->kv_heads;
-  p->shape = sv::attend_shape(d->dtype, d->head_dim);
+  p->shape = attend_shape(*d);
   const int64_t cap = std::min<int64_t>(static_cast<int64_t>(d->max_blocks) * d->block_size,
                                         INT32_MAX);
   p->cap = static_cast<int32_t>(cap);
@@ -151,22 +175,6 @@ int32_t make_attend_plan(const spec_kv_attention_desc* d, AttendPlan* p) {
 }
 
 }  // namespace
-
-namespace sv {
-
-// Two workgroups per CU to share 256 CUs evenly; a split below 8 units (256
-// keys) costs more in its partial result than it gains.
-AttendShape attend_shape(int dtype, int D) {
-  (void)dtype;
-  AttendShape s{};
-  s.mt = D <= 64 ? kRowsMT64 : D <= 128 ? kRowsMT128 : kRowsMT256;
-  s.kt = kRowsKT;
-  s.wgs = 1024;
-  s.min_units = 8;
-  return s;
-}
-
-}  // namespace sv
 
 extern "C" {
 
@@ -344,7 +352,11 @@ int32_t kv_paged_attention(const spec_kv_attention_desc* desc, const void* q,
     a.part_o = reinterpret_cast<float*>(ws + 256 + p.info_bytes + p.ml_bytes);
   }
   hipStream_t st = static_cast<hipStream_t>(hip_stream);
-  hipError_t err = sv::launch_attend_rows(a, d.dtype, st);
+  hipError_t err;
+  if (!p.shape.matrix) err = sv::launch_attend_rows(a, d.dtype, st);
+  else if (a.D == 64) err = sv::launch_attend_d64(a, d.dtype, p.shape.mt, st);
+  else if (a.D == 128) err = sv::launch_attend_d128(a, d.dtype, p.shape.mt, st);
+  else err = sv::launch_attend_d256(a, d.dtype, p.shape.mt, st);
   if (err != hipSuccess) return device_error(err, "paged attention launch");
   if (p.max_slots > 0) {
     err = sv::launch_attend_join(a, d.dtype, p.shape.mt, st);
