@@ -25,7 +25,8 @@ FLAGS = [
 
 def _cmd(out, extra):
     srcs = sorted(glob.glob(os.path.join(HERE, "csrc", "*.hip")))
-    return [HIPCC, *FLAGS, *extra, "-I" + os.path.join(ROOT, "include"),
+    # -parallel-jobs: device passes of one file side by side
+    return [HIPCC, *FLAGS, "-parallel-jobs=4", *extra, "-I" + os.path.join(ROOT, "include"),
             "-I" + os.path.join(HERE, "csrc"), *srcs, "-o", out + ".tmp"]
 
 

@@ -94,6 +94,10 @@ size_t pad256(size_t n) { return (n + 255) / 256 * 256; }
 // The kernel for a call: the matrix-core one where types and head size have it,
 // with the smallest tile that takes the rows of one sequence and key head
 // (rows: the caller's max_new, or the batch's mean, times the heads of a group).
+// wgs: items to aim at where keys are split, one for each workgroup the chip
+// holds.  A split costs a row 8 bytes of partial result per element, written
+// and read, a position 4 of cache: at 16 positions or more per row that stays
+// below an eighth.
 sv::AttendShape attend_shape(const spec_kv_attention_desc& d) {
   sv::AttendShape s{};
   const int D = d.head_dim;
@@ -102,10 +106,11 @@ sv::AttendShape attend_shape(const spec_kv_attention_desc& d) {
     const int64_t mean = d.batch > 0 ? (static_cast<int64_t>(d.tokens) + d.batch - 1) / d.batch : 1;
     const int64_t n = std::min<int64_t>(d.max_new > 0 ? d.max_new : mean, d.tokens);
     const int64_t rows = n * (d.heads / d.kv_heads);
-    s.mt = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
-    s.kt = D == 256 ? 32 : 64;
-    s.wgs = 1024;
-    s.min_units = 256 / s.kt;
+    s.mt = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 || D == 256 ? 64 : 128;
+    s.kt = s.mt == 128 ? 64 : 32;
+    s.wgs = 512;
+    s.min_units = static_cast<int32_t>(std::max<int64_t>(64, 16 * std::min<int64_t>(rows, s.mt)) /
+                                       s.kt);
   } else {
     s.mt = D <= 64 ? sv::kRowsMT64 : D <= 128 ? sv::kRowsMT128 : sv::kRowsMT256;
     s.kt = sv::kRowsKT;

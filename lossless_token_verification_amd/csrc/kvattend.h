@@ -51,9 +51,13 @@ __device__ __forceinline__ uint64_t wave_prefix(uint64_t v) {
   return v;
 }
 
+constexpr int kLengthClasses = 32;
+
 template <int WAVES>
 struct AttendPlanShared {
   uint64_t sum[2][WAVES];
+  uint64_t cls[kLengthClasses];
+  int32_t longest[WAVES];
   AttendItem item;
   int32_t found;
 };
@@ -64,51 +68,103 @@ struct AttendPlanShared {
 // A sequence's keys are cut into splits of about S units, where S is what
 // spreads the call's units evenly over want_items workgroups and at least
 // min_units: with many tiles nothing is split, with few rows the key axis
-// fills the chip.  sum tiles * ceil(units / S) <= want_items + tiles, which
-// bounds the launch; the sequences that are split have units > S, so they use
-// at most 2 * want_items partial slots.  Every workgroup makes these sums
-// itself (two prefix passes over the batch, from cache), which costs less than
-// the launch that a separate planning kernel would be.
+// fills the chip.  sum tiles * ceil(units / S) <= want_items where that leaves
+// room beside one split a tile (one workgroup too many of equal ones costs a
+// whole round: 461 against 322 us at B = 4, 110k positions), and never more
+// than want_items + tiles, which bounds the launch; the sequences that are
+// split have units > S, so they use at most 2 want_items partial slots.  Items are numbered from the longest class of splits to the
+// shortest, so that the last workgroups to start are the short ones (B = 256,
+// 512 to 4096 positions: 474 -> 437 us).  Every workgroup makes these sums
+// itself (passes over the batch from cache), which costs less than the launch
+// that a separate planning kernel would be.
 template <int MT, int KT, int WAVES>
 __device__ __forceinline__ bool attend_find(const AttendArgs& a, int x, bool count_slots,
                                             AttendPlanShared<WAVES>& sh, AttendItem& it) {
   constexpr int NT = WAVES * kWave;
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
-  int64_t S = INT32_MAX;
-  if (a.max_slots > 0) {
-    uint64_t units = 0;
-    for (int b = tid; b < a.B; b += NT) {
-      const AttendSeq s = attend_seq<MT, KT>(a, b);
-      units += static_cast<uint64_t>(s.tiles) * s.units;
-    }
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1)
-      units += __shfl_xor(static_cast<unsigned long long>(units), o, kWave);
-    if (WAVES > 1) {
-      if (lane == 0) sh.sum[0][wave] = units;
-      __syncthreads();
-      units = 0;
-#pragma unroll
-      for (int w = 0; w < WAVES; ++w) units += sh.sum[0][w];
-    }
-    S = max(static_cast<int64_t>(a.min_units),
-            static_cast<int64_t>((units + a.want_items - 1) / a.want_items));
-  }
+  if (tid < kLengthClasses) sh.cls[tid] = 0;
   if (tid == 0) sh.found = 0;
-  uint64_t carry = 0;   // (items << 32) + slots of the sequences before this chunk
-  for (int c = 0; c < a.B; c += NT) {
+  uint64_t units = 0, tiles = 0;
+  int longest = 0;
+  for (int b = tid; b < a.B; b += NT) {
+    const AttendSeq s = attend_seq<MT, KT>(a, b);
+    tiles += s.tiles;
+    units += static_cast<uint64_t>(s.tiles) * s.units;
+    if (s.tiles > 0) longest = max(longest, s.units);
+  }
+  if (a.B > 1) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) {
+      tiles += __shfl_xor(static_cast<unsigned long long>(tiles), o, kWave);
+      units += __shfl_xor(static_cast<unsigned long long>(units), o, kWave);
+      longest = max(longest, __shfl_xor(longest, o, kWave));
+    }
+    if (WAVES > 1) {
+      if (lane == 0) {
+        sh.sum[0][wave] = units;
+        sh.sum[1][wave] = tiles;
+        sh.longest[wave] = longest;
+      }
+      __syncthreads();
+      units = tiles = 0;
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) {
+        units += sh.sum[0][w];
+        tiles += sh.sum[1][w];
+        longest = max(longest, sh.longest[w]);
+      }
+    }
+  }
+  int S = INT32_MAX;
+  if (a.max_slots > 0) {
+    const int64_t room = static_cast<int64_t>(a.want_items) - static_cast<int64_t>(tiles);
+    const int over = max(static_cast<int>(max(room, static_cast<int64_t>(0))),
+                         (a.want_items + 1) / 2);
+    // a little over units / over, at least it
+    const float share = static_cast<float>(units) * 1.0001f / static_cast<float>(over);
+    S = max(a.min_units, share < 1e9f ? static_cast<int>(share) + 1 : INT32_MAX);
+  }
+  // splits of a sequence, their length's class and its (items << 32) + slots
+  const int top = min(longest, S);
+  auto shape = [&](const AttendSeq& s, int& splits, int& cls) -> uint64_t {
+    splits = s.units > S ? static_cast<int>((static_cast<uint32_t>(s.units) + S - 1) / S) : 1;
+    const float len = static_cast<float>(s.units) / static_cast<float>(splits);
+    const int c = static_cast<int>(len * kLengthClasses / static_cast<float>(top + 1));
+    cls = kLengthClasses - 1 - min(max(c, 0), kLengthClasses - 1);
+    const uint64_t items = static_cast<uint64_t>(s.tiles) * splits;
+    return (items << 32) + (splits > 1 ? items : 0);
+  };
+  int my_cls = 0;
+  uint64_t carry = 0, all = 0;   // (items << 32) + slots before this class, of the call
+  if (a.B > 1) {
+    for (int b = tid; b < a.B; b += NT) {
+      int splits, cls;
+      const uint64_t mine = shape(attend_seq<MT, KT>(a, b), splits, cls);
+      if (mine) atomicAdd(reinterpret_cast<unsigned long long*>(&sh.cls[cls]),
+                          static_cast<unsigned long long>(mine));
+    }
+    __syncthreads();
+    const uint64_t n = lane < kLengthClasses ? sh.cls[lane] : 0;
+    const uint64_t to = wave_prefix(n);
+    const uint64_t with = __ballot(static_cast<int64_t>(to >> 32) > x);
+    all = __shfl(static_cast<unsigned long long>(to), kWave - 1, kWave);
+    my_cls = with ? __builtin_ctzll(with) : -1;
+    carry = with ? __shfl(static_cast<unsigned long long>(to - n), my_cls, kWave) : 0;
+  }
+  for (int c = 0; c < a.B && my_cls >= 0; c += NT) {
     const int b = c + tid;
     AttendSeq s{};
     int splits = 1;
     uint64_t mine = 0;
     if (b < a.B) {
       s = attend_seq<MT, KT>(a, b);
-      if (s.units > S) splits = static_cast<int>((s.units + S - 1) / S);
-      const uint64_t items = static_cast<uint64_t>(s.tiles) * splits;
-      mine = (items << 32) + (splits > 1 ? items : 0);
+      int cls;
+      mine = shape(s, splits, cls);
+      if (a.B == 1) all = mine;
+      else if (cls != my_cls) mine = 0;
     }
-    uint64_t v = wave_prefix(mine);
-    uint64_t all = 0, before = carry;
+    const uint64_t v = wave_prefix(mine);
+    uint64_t here = 0, before = carry;
     if (WAVES > 1) {
       __syncthreads();
       if (lane == kWave - 1) sh.sum[1][wave] = v;
@@ -116,18 +172,19 @@ __device__ __forceinline__ bool attend_find(const AttendArgs& a, int x, bool cou
 #pragma unroll
       for (int w = 0; w < WAVES; ++w) {
         if (w < wave) before += sh.sum[1][w];
-        all += sh.sum[1][w];
+        here += sh.sum[1][w];
       }
     } else {
-      all = __shfl(static_cast<unsigned long long>(v), kWave - 1, kWave);
+      here = __shfl(static_cast<unsigned long long>(v), kWave - 1, kWave);
     }
     before += v - mine;
-    carry += all;
+    carry += here;
     const int64_t y = x - static_cast<int64_t>(before >> 32);
     if (y >= 0 && y < static_cast<int64_t>(mine >> 32)) {
       // the tiles of a sequence from its last (with the most keys) to its first
-      const int split = static_cast<int>(y % splits);
-      const int tile = s.tiles - 1 - static_cast<int>(y / splits);
+      const uint32_t q = static_cast<uint32_t>(y) / static_cast<uint32_t>(splits);
+      const int split = static_cast<int>(static_cast<uint32_t>(y) - q * splits);
+      const int tile = s.tiles - 1 - static_cast<int>(q);
       const int rows_all = s.n * a.group;
       AttendItem r;
       r.b = b;
@@ -142,7 +199,8 @@ __device__ __forceinline__ bool attend_find(const AttendArgs& a, int x, bool cou
       r.key_hi = static_cast<int32_t>(max(hi, static_cast<int64_t>(r.key_lo)));
       const int f = r.key_lo / KT;
       const int e = r.key_hi > r.key_lo ? (r.key_hi - 1) / KT + 1 : f;
-      const int len = (e - f + splits - 1) / splits;
+      const int len = static_cast<int>(static_cast<uint32_t>(e - f + splits - 1) /
+                                       static_cast<uint32_t>(splits));
       r.u0 = min(e, f + split * len);
       r.u1 = min(e, r.u0 + len);
       r.split = split;
@@ -151,10 +209,10 @@ __device__ __forceinline__ bool attend_find(const AttendArgs& a, int x, bool cou
       sh.item = r;
       sh.found = 1;
     }
-    if (static_cast<int64_t>(carry >> 32) > x && !count_slots) break;
+    if (static_cast<int64_t>(carry >> 32) > x) break;
   }
-  if (count_slots && tid == 0)
-    *a.slot_count = static_cast<int32_t>(min(static_cast<uint32_t>(carry),
+  if (count_slots && tid == 0)   // (thread 0 has the one sequence where B = 1)
+    *a.slot_count = static_cast<int32_t>(min(static_cast<uint32_t>(all),
                                              static_cast<uint32_t>(a.max_slots)));
   __syncthreads();
   if (!sh.found) return false;

@@ -20,10 +20,10 @@
 // relative to their size in both types.
 //
 // K and V units go from the pages straight into LDS (16-byte direct loads, no
-// register stage), one unit ahead in the other of two buffers; rows are
-// permuted by 16-byte vectors (swz_k, swz_v) so that the operand reads of
-// either product spread over all banks.  A row's page comes from the block
-// table one unit before that.
+// register stage), NB - 1 units ahead in a ring of NB buffers; rows are permuted
+// by 16-byte vectors (swz_k, swz_v) so that the operand reads of either product
+// spread over all banks.  A row's page comes from the block table NB units
+// before its loads, so that no wait for a table entry drains the ring.
 #pragma once
 
 #include <type_traits>
@@ -97,43 +97,76 @@ __device__ __forceinline__ int fresh(int x) {
   return x;
 }
 
-// RW: query rows per wavefront (16 or 32, the matrix instruction's width).  WR
-// wavefronts take different rows of a unit, WK different positions.
-template <typename T_, int D_, int RW_, int WR_, int WK_, int KT_>
+// RW: query rows per wavefront (16 or 32, the matrix instruction's width), W
+// wavefronts with different rows; units of KT positions in a ring of NB buffers.
+template <typename T_, int D_, int RW_, int W_, int KT_, int NB_>
 struct AttendCfg {
   using T = T_;
-  static constexpr int D = D_, RW = RW_, WR = WR_, WK = WK_, KT = KT_;
-  static constexpr int W = WR * WK, MT = RW * WR;
-  static constexpr int KW = KT / WK;               // positions per wavefront and unit
+  static constexpr int D = D_, RW = RW_, W = W_, KT = KT_, NB = NB_;
+  static constexpr int MT = RW * W;
   static constexpr int NV = D / 8;                 // vectors of a row
   static constexpr int RPL = kWave / NV;           // rows of one direct load
-  static constexpr int LOADS = KT / RPL / W;       // of K and of V, per wavefront
+  static constexpr int LOADS = KT / RPL / W;       // of K and of V, per wavefront and unit
+  static constexpr int SUPER = KT * NB;            // positions of a turn of the ring
+  static constexpr int IDS = SUPER / kWave;        // table lookups per lane and turn
   static constexpr int QS = RW == 32 ? D / 16 : D / 32;     // steps of the first product
-  static constexpr int ST = KW / RW;               // its result tiles
+  static constexpr int ST = KT / RW;               // its result tiles
   static constexpr int SR = RW == 32 ? 16 : 4;     // registers of a result tile
-  static constexpr int PS = RW == 32 ? KW / 16 : KW / 32;   // steps of the second product
+  static constexpr int PS = RW == 32 ? KT / 16 : KT / 32;   // steps of the second product
   static constexpr int OT = D / RW;                // its result tiles
-  static_assert(KT % (RPL * W) == 0 && KW % 32 == 0 && KT <= kWave, "unit shape");
+  // Nontemporal direct loads where a sequence has one tile, which reads a page
+  // once (B = 256 verification 511 -> 474 us; at head_dim 256 sequences of many
+  // tiles come with 64 rows too, and lose a tenth by them).
+  static constexpr bool kOnce = MT <= (D == 256 ? 32 : 64);
+  static_assert(KT % (RPL * W) == 0 && KT % 32 == 0 && KT <= kWave && SUPER % kWave == 0,
+                "unit shape");
 };
 
 constexpr float kSlack = 8.0f;
 
+typedef const void __attribute__((address_space(1)))* gptr_t;
+typedef void __attribute__((address_space(3)))* lptr_t;
+// 16 bytes per lane from memory straight into LDS (from `l` on, in lane order).
+template <bool kOnce>
+__device__ __forceinline__ void load_lds(const void* g, void* l) {
+  if constexpr (kOnce) __builtin_amdgcn_global_load_lds((gptr_t)g, (lptr_t)l, 16, 0, 2);
+  else __builtin_amdgcn_global_load_lds((gptr_t)g, (lptr_t)l, 16, 0, 0);
+}
+
+// Waits until at most N of the wavefront's vector-memory operations are under
+// way and none of its LDS reads.  The builtin (counts in the hardware's fields:
+// vector memory in bits 0-3 and 14-15, LDS in bits 8-11) is known to the
+// compiler, which then adds no wait of its own for the loads it covers.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | ((N >> 4) << 14));
+  asm volatile("" ::: "memory");
+}
+
+// The bounds name four wavefronts for every W: with the LDS of two workgroups
+// to a CU that is two wavefronts to a SIMD, for which the compiler keeps to 256
+// registers and forms the products in them (given more, it moves every
+// accumulator through the other half of the file in each unit).
 template <class C>
-__global__ __launch_bounds__(C::W * kWave) __attribute__((amdgpu_waves_per_eu(C::W >= 4 && C::D < 256 ? 2 : 1))) void
+__global__ __launch_bounds__(4 * kWave) __attribute__((amdgpu_waves_per_eu(2))) void
 attend_mfma_kernel(AttendArgs a) {
   using T = typename C::T;
-  constexpr int D = C::D, RW = C::RW, KT = C::KT, KW = C::KW, NV = C::NV, RPL = C::RPL;
-  constexpr int SR = C::SR, ST = C::ST, OT = C::OT, PS = C::PS, QS = C::QS;
+  constexpr int D = C::D, RW = C::RW, KT = C::KT, NB = C::NB, NV = C::NV, RPL = C::RPL;
+  constexpr int SR = C::SR, ST = C::ST, OT = C::OT, PS = C::PS, QS = C::QS, IDS = C::IDS;
   typedef typename std::conditional<RW == 32, f32x16, f32x4>::type acc_t;
-  // each buffer its own LDS object: the compiler then knows that a direct load
-  // into one does not change the other, and does not wait for it
-  __shared__ __attribute__((aligned(1024))) uint16_t sk0[KT * D], sk1[KT * D];
-  __shared__ __attribute__((aligned(1024))) uint16_t sv0[KT * D], sv1[KT * D];
+  // K rows, then V rows of a unit.  Each buffer its own LDS object: the compiler
+  // then knows that a direct load into one does not change the others, and does
+  // not wait for it.
+  constexpr int kV = KT * D;   // where the V rows start
+  __shared__ __attribute__((aligned(1024))) uint16_t sb0[2 * kV], sb1[2 * kV];
+  __shared__ __attribute__((aligned(1024))) uint16_t sb2[NB > 2 ? 2 * kV : 1];
+  __shared__ __attribute__((aligned(1024))) uint16_t sb3[NB > 3 ? 2 * kV : 1];
+  // looked-up table entries of the ring's next turn, a copy per wavefront
+  __shared__ __attribute__((aligned(256))) int32_t sid[C::W * C::SUPER];
   __shared__ AttendPlanShared<C::W> plan;
-  __shared__ float smerge[C::WK > 1 ? 2 * C::WR * RW : 1];
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-  const int wr = wave / C::WK, wk = wave - wr * C::WK;
   const int x = blockIdx.x / a.kv_heads, h = blockIdx.x - x * a.kv_heads;
   AttendItem it;
   if (!attend_find<C::MT, KT, C::W>(a, x, a.max_slots > 0 && blockIdx.x == 0, plan, it)) return;
@@ -141,58 +174,83 @@ attend_mfma_kernel(AttendArgs a) {
 
   // this lane's query row; rows past the tile repeat its last one
   const int hi_lane = RW == 32 ? lane >> 5 : lane >> 4;   // which part of k a lane holds
-  const int row = wr * RW + (lane & (RW - 1));
-  int token, head;
-  attend_row(a, it.token0, it.row0 + min(row, it.rows - 1), h, token, head);
-  const int pos = it.pos0 + token - it.token0;
-  const int key_hi = min(pos, it.key_hi - 1);            // last and first position it may see
-  const int key_lo = a.window > 0 ? max(pos - a.window + 1, 0) : 0;
-  // positions every row of the tile may see: units inside need no mask
-  const int all_hi = min(it.pos0 + fast_div(it.row0, a.grp), it.key_hi - 1);
-  const int all_lo =
-      a.window > 0 ? it.pos0 + fast_div(it.row0 + it.rows - 1, a.grp) - a.window + 1 : 0;
-
+  const int row = wave * RW + (lane & (RW - 1));
+  // the positions it sees: see_span of them from see_lo on, and that one
+  int see_lo;
+  uint32_t see_span;
   u32x4 qf[QS];
   {
+    int token, head;
+    attend_row(a, it.token0, it.row0 + min(row, it.rows - 1), h, token, head);
+    const int pos = it.pos0 + token - it.token0;
+    const int key_last = min(pos, it.key_hi - 1);
+    const int key_first = a.window > 0 ? max(pos - a.window + 1, 0) : 0;
+    see_lo = key_last >= key_first ? key_first : INT32_MAX;
+    see_span = key_last >= key_first ? key_last - key_first : 0;
     const T* qr = static_cast<const T*>(a.q) + token * a.q_stride + static_cast<int64_t>(head) * D;
 #pragma unroll
     for (int s = 0; s < QS; ++s)
       qf[s] = reinterpret_cast<const u32x4*>(qr)[s * (RW == 32 ? 2 : 4) + hi_lane];
   }
+  // positions every row of the tile may see: units inside need no mask
+  const int all_hi = min(it.pos0 + fast_div(it.row0, a.grp), it.key_hi - 1);
+  const int all_lo =
+      a.window > 0 ? it.pos0 + fast_div(it.row0 + it.rows - 1, a.grp) - a.window + 1 : 0;
 
   const int32_t* table = a.table + static_cast<int64_t>(it.b) * a.max_blocks;
   const int64_t head_off = static_cast<int64_t>(h) * a.block_size;
-  // Lane l looks up position l of a unit: its element offset in the caches, and
+  // Lane l looks up position base + l: its element offset in the caches, and
   // whether there is such a page.  Positions outside the item's range read the
   // nearest one inside (and are masked); a missing page reads block 0.
-  auto lookup = [&](int u) -> int {
-    const int key = min(max(u * KT + (lane & (KT - 1)), it.key_lo), it.key_hi - 1);
-    return table[fast_div(key, a.bs)];
-  };
-  auto offset = [&](int u, int id) -> int64_t {
-    const int key = min(max(u * KT + (lane & (KT - 1)), it.key_lo), it.key_hi - 1);
+  auto nearest = [&](int base) { return min(max(base + lane, it.key_lo), it.key_hi - 1); };
+  auto entry = [&](int base) { return table + fast_div(nearest(base), a.bs); };
+  auto offset = [&](int base, int id) -> int64_t {
+    const int key = nearest(base);
     const int r = key - fast_div(key, a.bs) * a.block_size;
     const int safe = id >= 0 && id < a.num_blocks ? id : 0;
     return safe * a.block_stride + (head_off + r) * D;
   };
   auto paged = [&](int id) -> uint64_t { return __ballot(id >= 0 && id < a.num_blocks); };
 
-  typedef const void __attribute__((address_space(1)))* gptr_t;
-  typedef void __attribute__((address_space(3)))* lptr_t;
   const T* kb = static_cast<const T*>(a.k);
   const T* vb = static_cast<const T*>(a.v);
   // lane part of a direct load: row q of its RPL rows, vector `slot` of that row
   const int lq = lane / NV, lslot = lane & (NV - 1);
-  auto load_unit = [&](int64_t off, uint16_t* sk, uint16_t* sv) {
-    const int lk = fresh(lslot ^ swz_k<D>(lq)), lv = fresh(lslot ^ swz_v<D>(lq));
-#pragma unroll
+  const bool whole_rows = a.block_size % RPL == 0;   // a load's rows share a page
+  // Loads the unit at position `base`; off: offsets of 64 positions, the unit's
+  // from lane `from` on.  Inside the item's range, with whole pages of rows, a
+  // load's address is one lane's offset plus a lane constant, so the offset
+  // moves through scalar registers; otherwise every lane fetches its row's.
+  auto load_unit = [&](int base, int64_t off, int from, uint16_t* sb) {
+    constexpr int kUnroll = C::LOADS > 8 ? 4 : C::LOADS;
+    int lk = lslot ^ swz_k<D>(lq), lv = lslot ^ swz_v<D>(lq);
+    if (D == 256) {   // many different lane parts: formed at each load
+      lk = fresh(lk);
+      lv = fresh(lv);
+    }
+    if (whole_rows && base >= it.key_lo && base + KT <= it.key_hi) {
+      const int lo = static_cast<int>(off), hi = static_cast<int>(off >> 32);
+      const uint32_t lane_row = lq * D * 2;
+#pragma unroll kUnroll
+      for (int i = 0; i < C::LOADS; ++i) {
+        const int j = wave + i * C::W;               // which RPL rows
+        const uint32_t r0 = __builtin_amdgcn_readlane(lo, from + j * RPL);
+        const uint32_t r1 = __builtin_amdgcn_readlane(hi, from + j * RPL);
+        const int64_t ro = static_cast<int64_t>((static_cast<uint64_t>(r1) << 32) | r0);
+        const uint32_t ko = lane_row + (lk ^ swz_k<D>(j * RPL)) * 16;
+        const uint32_t vo = lane_row + (lv ^ swz_v<D>(j * RPL)) * 16;
+        load_lds<C::kOnce>(reinterpret_cast<const char*>(kb + ro) + ko, sb + j * 512);
+        load_lds<C::kOnce>(reinterpret_cast<const char*>(vb + ro) + vo, sb + kV + j * 512);
+      }
+      asm volatile("; scalar addresses");   // keeps the two forms from being merged
+      return;
+    }
+#pragma unroll kUnroll
     for (int i = 0; i < C::LOADS; ++i) {
-      const int j = wave + i * C::W;                 // which RPL rows
-      const int64_t ro = __shfl(static_cast<long long>(off), j * RPL + lq, kWave);
-      __builtin_amdgcn_global_load_lds((gptr_t)(kb + ro + (lk ^ swz_k<D>(j * RPL)) * 8),
-                                       (lptr_t)(sk + j * 512), 16, 0, 0);
-      __builtin_amdgcn_global_load_lds((gptr_t)(vb + ro + (lv ^ swz_v<D>(j * RPL)) * 8),
-                                       (lptr_t)(sv + j * 512), 16, 0, 0);
+      const int j = wave + i * C::W;
+      const int64_t ro = __shfl(static_cast<long long>(off), from + j * RPL + lq, kWave);
+      load_lds<C::kOnce>(kb + ro + (lk ^ swz_k<D>(j * RPL)) * 8, sb + j * 512);
+      load_lds<C::kOnce>(vb + ro + (lv ^ swz_v<D>(j * RPL)) * 8, sb + kV + j * 512);
     }
   };
 
@@ -202,21 +260,21 @@ attend_mfma_kernel(AttendArgs a) {
 
   // Operand reads.  Byte offset of the lane's part at step / tile 0; the others
   // differ by an xor inside the row and by whole rows.
-  const int krow = wk * KW + (lane & (RW - 1));
+  const int krow = lane & (RW - 1);
   const int koff = krow * (D * 2) + ((hi_lane ^ swz_k<D>(krow)) << 4);
   constexpr int kKStep = RW == 32 ? 32 : 64;       // bytes of a row per step
   // V, k order of the operand = positions of the result registers.  32 wide:
   // 4h + i and 8 + 4h + i of 16; 16 wide: 4g + i and 16 + 4g + i of 32.  A
   // transposed read gives lane n of 16 element n of 4 rows; lane n fetches row
   // n / 4, elements 4 (n % 4) ..
-  const int vrow = wk * KW + 4 * hi_lane + ((lane & 15) >> 2);
+  const int vrow = 4 * hi_lane + ((lane & 15) >> 2);
   const int vvec = (RW == 32 ? ((lane >> 4) & 1) * 2 : 0) + ((lane & 3) >> 1);
   const int voff = vrow * (D * 2) + ((vvec ^ swz_v<D>(vrow)) << 4) + (lane & 1) * 8;
   constexpr int kVTile = RW * 2;                    // bytes of a row per result tile
   constexpr int kVSpan = RW == 32 ? 16 : 32;        // positions per step
-  auto vread = [&](const uint16_t* sv, int vo, int s, int ot) -> u32x4 {
+  auto vread = [&](const uint16_t* sb, int vo, int s, int ot) -> u32x4 {
     typedef __attribute__((address_space(3))) s16x4* tr_t;
-    const char* p = reinterpret_cast<const char*>(sv) + (vo ^ (ot * kVTile)) + s * kVSpan * D * 2;
+    const char* p = reinterpret_cast<const char*>(sb + kV) + (vo ^ (ot * kVTile)) + s * kVSpan * D * 2;
     const s16x4 x0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((tr_t)(p));
     const s16x4 x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((tr_t)(p + kVSpan * D));
     typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -228,36 +286,44 @@ attend_mfma_kernel(AttendArgs a) {
     else return Mma<T>::mma16(x, y, z);
   };
 
-  // One unit.  CAREFUL: values that are not finite reach only the rows that see
-  // their position (0 times infinity is NaN in a product over all positions).
-  auto compute = [&](const uint16_t* sk, const uint16_t* sv, int u, uint64_t pages, auto careful) {
-    constexpr bool kCareful = decltype(careful)::value;
+  // One unit.  The scores and weights of its positions: pf gets the weights in
+  // the second product's operand form, `scale` is called with the factor of the
+  // accumulators where the maximum moves.  pages: which positions have a page.
+  auto weigh = [&](const uint16_t* sb, int u, uint64_t pages, u32x4 (&pf)[PS], auto always_mask,
+                   auto scale) {
     acc_t st[ST];
-    const int ko = fresh(koff), vo = fresh(voff);
+    const int ko = fresh(koff);
 #pragma unroll
     for (int t = 0; t < ST; ++t) {
 #pragma unroll
       for (int r = 0; r < SR; ++r) st[t][r] = 0.0f;
 #pragma unroll
       for (int s = 0; s < QS; ++s)
-        st[t] = mma(*reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(sk) +
+        st[t] = mma(*reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(sb) +
                                                     (ko ^ (s * kKStep)) + t * RW * D * 2),
                     qf[s], st[t]);
     }
     // position of register r of tile t, less the lane's part 4 * hi_lane
     auto at = [&](int t, int r) { return t * RW + (RW == 32 ? (r >> 2) * 8 + (r & 3) : r); };
-    const int base = u * KT + wk * KW + 4 * hi_lane;
-    const uint64_t every = KT == 64 ? ~uint64_t{0} : (uint64_t{1} << (KT & 63)) - 1;
-    const bool masked = u * KT + KT - 1 > all_hi || u * KT < all_lo || (pages & every) != every;
-    const uint64_t seen = pages >> (wk * KW + 4 * hi_lane);
-    if (masked || kCareful) {
+    constexpr uint64_t kEvery = KT == 64 ? ~uint64_t{0} : (uint64_t{1} << (KT & 63)) - 1;
+    pages &= kEvery;
+    if (decltype(always_mask)::value || u * KT + KT - 1 > all_hi || u * KT < all_lo) {
+      // key_lo <= position <= key_hi as one unsigned comparison; a row that sees
+      // nothing has span 0 at a position that is none
+      const int d = u * KT + 4 * hi_lane - see_lo;
 #pragma unroll
       for (int t = 0; t < ST; ++t)
 #pragma unroll
-        for (int r = 0; r < SR; ++r) {
-          const int key = base + at(t, r);
-          if (key > key_hi || key < key_lo || !((seen >> at(t, r)) & 1)) st[t][r] = -INFINITY;
-        }
+        for (int r = 0; r < SR; ++r)
+          st[t][r] = static_cast<uint32_t>(d + at(t, r)) > see_span ? -INFINITY : st[t][r];
+    }
+    if (pages != kEvery) {
+      const uint64_t here = pages >> (4 * hi_lane);
+#pragma unroll
+      for (int t = 0; t < ST; ++t)
+#pragma unroll
+        for (int r = 0; r < SR; ++r)
+          st[t][r] = (here >> at(t, r)) & 1 ? st[t][r] : -INFINITY;
     }
     float mx = st[0][0];
 #pragma unroll
@@ -272,13 +338,9 @@ attend_mfma_kernel(AttendArgs a) {
       const float f = __builtin_amdgcn_exp2f(m - (mn == -INFINITY ? 0.0f : mn));
       m = mn;
       l *= f;
-#pragma unroll
-      for (int t = 0; t < OT; ++t)
-#pragma unroll
-        for (int r = 0; r < SR; ++r) o[t][r] *= f;
+      scale(f);
     }
     const float ref = m == -INFINITY ? 0.0f : m;
-    u32x4 pf[PS];
     float sum = 0.0f;
 #pragma unroll
     for (int t = 0; t < ST; ++t)
@@ -291,154 +353,198 @@ attend_mfma_kernel(AttendArgs a) {
         else pf[t / 2][(t & 1) * 2 + r / 2] = pack2<T>(p0, p1);
       }
     l += sum;
+  };
+  auto compute = [&](const uint16_t* sb, int u, uint64_t pages) {
+    u32x4 pf[PS];
+    weigh(sb, u, pages, pf, std::false_type{}, [&](float f) {
+#pragma unroll
+      for (int t = 0; t < OT; ++t)
+#pragma unroll
+        for (int r = 0; r < SR; ++r) o[t][r] *= f;
+    });
+    const int vo = fresh(voff);
 #pragma unroll
     for (int s = 0; s < PS; ++s)
 #pragma unroll
-      for (int t = 0; t < OT; ++t) {
-        u32x4 vf = vread(sv, vo, s, t);
-        if constexpr (!kCareful) {
-          o[t] = mma(vf, pf[s], o[t]);
-        } else {
-          u32x4 clean = vf, rest;
+      for (int t = 0; t < OT; ++t) o[t] = mma(vread(sb, vo, s, t), pf[s], o[t]);
+  };
+  // One unit's product for the result tile at vt, with values that are not finite
+  // reaching only the rows that see their position (0 times infinity is NaN in
+  // a product over all positions): they are left out of the product, and each
+  // position that has one is multiplied alone, for the rows that see it.
+  auto compute_careful = [&](const uint16_t* sb, int u, uint64_t pages, int vt, acc_t& x) {
+    u32x4 pf[PS];
+    weigh(sb, u, pages, pf, std::true_type{}, [&](float f) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t lo = (vf[i] & Mma<T>::kExp) == Mma<T>::kExp ? 0xffffu : 0u;
-            const uint32_t hi = ((vf[i] >> 16) & Mma<T>::kExp) == Mma<T>::kExp ? 0xffff0000u : 0u;
-            clean[i] = vf[i] & ~(lo | hi);
-            rest[i] = vf[i] & (lo | hi);
-          }
-          o[t] = mma(clean, pf[s], o[t]);
-          if (__any((rest.x | rest.y | rest.z | rest.w) != 0u)) {
-            // one position at a time: the product of its values alone, for the
-            // rows that see it
-            constexpr int kSpan = RW == 32 ? 16 : 32;
-            for (int k = 0; k < kSpan; ++k) {
-              // operand element of position k: part (k >> 2), register pair
-              const int part = RW == 32 ? (k >> 2) & 1 : (k >> 2) & 3;
-              const int el = (k & 3) + (k >= kSpan / 2 ? 4 : 0);
-              u32x4 one;
+      for (int r = 0; r < SR; ++r) x[r] *= f;
+    });
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                one[i] = part == hi_lane && (el >> 1) == i
-                             ? rest[i] & ((el & 1) ? 0xffff0000u : 0xffffu) : 0u;
-              if (!__any((one.x | one.y | one.z | one.w) != 0u)) continue;
-              acc_t zero;
+    for (int s = 0; s < PS; ++s) {
+      const u32x4 vf = vread(sb, vt, s, 0);
+      u32x4 clean, rest;
 #pragma unroll
-              for (int r = 0; r < SR; ++r) zero[r] = 0.0f;
-              const acc_t add = mma(one, pf[s], zero);
-              const int in = wk * KW + s * kSpan + k, key = u * KT + in;
-              if (key <= key_hi && key >= key_lo && ((pages >> in) & 1)) {
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = (vf[i] & Mma<T>::kExp) == Mma<T>::kExp ? 0xffffu : 0u;
+        const uint32_t hi = ((vf[i] >> 16) & Mma<T>::kExp) == Mma<T>::kExp ? 0xffff0000u : 0u;
+        clean[i] = vf[i] & ~(lo | hi);
+        rest[i] = vf[i] & (lo | hi);
+      }
+      x = mma(clean, pf[s], x);
+      if (!__any((rest.x | rest.y | rest.z | rest.w) != 0u)) continue;
+      for (int k = 0; k < kVSpan; ++k) {
+        // position k of the step: operand part (k >> 2), element el of the lane
+        const int part = RW == 32 ? (k >> 2) & 1 : (k >> 2) & 3;
+        const int el = (k & 3) + (k >= kVSpan / 2 ? 4 : 0);
+        u32x4 one;
 #pragma unroll
-                for (int r = 0; r < SR; ++r) o[t][r] += add[r];
-              }
-            }
-          }
+        for (int i = 0; i < 4; ++i)
+          one[i] = part == hi_lane && (el >> 1) == i
+                       ? rest[i] & ((el & 1) ? 0xffff0000u : 0xffffu) : 0u;
+        if (!__any((one.x | one.y | one.z | one.w) != 0u)) continue;
+        acc_t zero;
+#pragma unroll
+        for (int r = 0; r < SR; ++r) zero[r] = 0.0f;
+        const acc_t add = mma(one, pf[s], zero);
+        const int in = s * kVSpan + k;
+        if (static_cast<uint32_t>(u * KT + in - see_lo) <= see_span && ((pages >> in) & 1)) {
+#pragma unroll
+          for (int r = 0; r < SR; ++r) x[r] += add[r];
         }
       }
+    }
   };
-  // All units of the item.  Unit u computes on buffer (u - u0) % 2 while unit
-  // u + 1 is loaded into the other and the pages of unit u + 2 are looked up;
-  // the barrier that ends a unit also ends the loads under way.
-  auto run = [&](auto careful) {
+  // The sum of a row's lanes, and the row's results.
+  auto row_sum = [&]() {
+    if (RW == 16) l += __shfl_xor(l, 16, kWave);
+    l += __shfl_xor(l, 32, kWave);
+  };
+  auto store_tile = [&](const acc_t& x, int t) {
+    if (row >= it.rows) return;
+    if (it.splits > 1) {
+      const int64_t p = (static_cast<int64_t>(it.slot) * a.kv_heads + h) * C::MT + row;
+      float* po = a.part_o + p * D + t * RW + 4 * hi_lane;
+#pragma unroll
+      for (int r = 0; r < SR; r += 4)
+        *reinterpret_cast<f32x4*>(po + r * 2) = f32x4{x[r], x[r + 1], x[r + 2], x[r + 3]};
+      return;
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    int token, head;
+    attend_row(a, it.token0, it.row0 + fresh(row), h, token, head);
+    T* po = static_cast<T*>(a.out) + (static_cast<int64_t>(token) * a.heads + head) * D + t * RW +
+            4 * hi_lane;
+#pragma unroll
+    for (int r = 0; r < SR; r += 4) {
+      typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+      *reinterpret_cast<u32x2*>(po + r * 2) =
+          u32x2{pack2<T>(x[r] * inv, x[r + 1] * inv), pack2<T>(x[r + 2] * inv, x[r + 3] * inv)};
+    }
+  };
+  auto store_sums = [&]() {
+    if (row >= it.rows || hi_lane != 0) return;
+    if (it.splits > 1) {
+      const int64_t p = (static_cast<int64_t>(it.slot) * a.kv_heads + h) * C::MT + row;
+      a.part_ml[p * 2] = m;
+      a.part_ml[p * 2 + 1] = l;
+    } else if (a.lse) {
+      int token, head;
+      attend_row(a, it.token0, it.row0 + fresh(row), h, token, head);
+      a.lse[static_cast<int64_t>(token) * a.heads + head] =
+          l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+    }
+  };
+  auto start = [&]() {
     m = -INFINITY;
     l = 0.0f;
 #pragma unroll
     for (int t = 0; t < OT; ++t)
 #pragma unroll
       for (int r = 0; r < SR; ++r) o[t][r] = 0.0f;
-    if (it.u0 >= it.u1) return;
-    int id = lookup(it.u0);
-    uint64_t pages = paged(id), pages_next = 0;
-    load_unit(offset(it.u0, id), sk0, sv0);
-    if (it.u0 + 1 < it.u1) id = lookup(it.u0 + 1);
-    auto step = [&](int u, const uint16_t* sk, const uint16_t* sv, uint16_t* nk, uint16_t* nv) {
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      __syncthreads();
-      if (u + 1 < it.u1) {
-        pages_next = paged(id);
-        load_unit(offset(u + 1, id), nk, nv);
-        if (u + 2 < it.u1) id = lookup(u + 2);
-      }
-      compute(sk, sv, u, pages, careful);
-      pages = pages_next;
-    };
-    int u = it.u0;
-    for (; u + 2 <= it.u1; u += 2) {
-      step(u, sk0, sv0, sk1, sv1);
-      step(u + 1, sk1, sv1, sk0, sv0);
-    }
-    if (u < it.u1) step(u, sk0, sv0, sk1, sv1);
   };
-  run(std::false_type{});
-  {
-    // anything not finite: again, carefully
+  start();
+  const int n_units = it.u1 - it.u0;
+  if (n_units > 0) {
+    // Step n computes unit n from buffer n % NB while units n + 1 .. n + NB - 1
+    // are under way.  Loads past the last unit read its nearest position again
+    // (one row), which keeps the number of loads under way a constant.  The table
+    // entries of turn q of the ring (units q NB ..) are loaded into LDS as well,
+    // one turn before their use, so that nothing but the counted waits waits.
+    uint16_t* const ring[4] = {sb0, sb1, sb2, sb3};
+    const int first = it.u0 * KT;
+    int32_t* const ids = sid + wave * C::SUPER;
+    int64_t off[IDS];
+    uint64_t mask[IDS], mask_next[IDS];
+    auto look = [&](int q) {          // starts the lookups of turn q
+#pragma unroll
+      for (int i = 0; i < IDS; ++i)
+        __builtin_amdgcn_global_load_lds((gptr_t)entry(first + q * C::SUPER + i * kWave),
+                                         (lptr_t)(ids + i * kWave), 4, 0, 0);
+    };
+    auto turn = [&](int q) {          // turn q, looked up, becomes the one that loads
+#pragma unroll
+      for (int i = 0; i < IDS; ++i) {
+        const int id = ids[i * kWave + lane];
+        mask_next[i] = paged(id);
+        off[i] = offset(first + q * C::SUPER + i * kWave, id);
+      }
+    };
+    auto load = [&](int n, int s) {   // unit n = unit s of the turn that loads
+      load_unit(first + n * KT, off[s * KT / kWave], s * KT % kWave, ring[s]);
+    };
+    look(0);
+    wait_loads<0>();
+    turn(0);
+    wait_loads<0>();                  // the entries are read before the next overwrite them
+    look(1);
+#pragma unroll
+    for (int s = 0; s < NB - 1; ++s) load(s, s);
+    for (int n = 0; n < n_units; n += NB) {
+#pragma unroll
+      for (int s = 0; s < NB; ++s) {
+        wait_loads<(NB - 2) * 2 * C::LOADS>();
+        if (C::W > 1) __builtin_amdgcn_s_barrier();
+        if (s == 0) {
+#pragma unroll
+          for (int i = 0; i < IDS; ++i) mask[i] = mask_next[i];
+        }
+        if (s == 1) turn(n / NB + 1);
+        load(n + s + NB - 1, (s + NB - 1) % NB);
+        if (s == 1) look(n / NB + 2);
+        if (n + s < n_units)
+          compute(ring[s], it.u0 + n + s, mask[s * KT / kWave] >> (s * KT % kWave));
+      }
+    }
+    // no load may still be under way when the workgroup gives its LDS back
+    wait_loads<0>();
+    // anything not finite: again, a result tile and a unit at a time, carefully
     float z = l * 0.0f;
 #pragma unroll
     for (int t = 0; t < OT; ++t)
 #pragma unroll
       for (int r = 0; r < SR; ++r) z = fmaf(o[t][r], 0.0f, z);
-    if (__syncthreads_or(!(z == 0.0f))) run(std::true_type{});
-  }
-
-  // the sums of a row's lanes, then of the wavefronts that shared its positions
-  if (RW == 16) l += __shfl_xor(l, 16, kWave);
-  l += __shfl_xor(l, 32, kWave);
-  if constexpr (C::WK > 1) {
-    static_assert(C::WK == 2 && C::WR == 1 && OT * SR * 4 <= KT * D * 2 / kWave, "merge space");
-    float* so = reinterpret_cast<float*>(sk0);
-    __syncthreads();
-    if (wk == 1) {
-#pragma unroll
-      for (int t = 0; t < OT; ++t)
-#pragma unroll
-        for (int r = 0; r < SR; ++r) so[(t * SR + r) * kWave + lane] = o[t][r];
-      if (hi_lane == 0) {
-        smerge[2 * row] = m;
-        smerge[2 * row + 1] = l;
+    if (__syncthreads_or(!(z == 0.0f))) {
+      for (int t = 0; t < OT; ++t) {
+        start();
+        acc_t x = o[0];
+        for (int u = it.u0; u < it.u1; ++u) {
+          const int page = *entry(u * KT);
+          load_unit(u * KT, offset(u * KT, page), 0, sb0);
+          wait_loads<0>();
+          __syncthreads();
+          compute_careful(sb0, u, paged(page), voff ^ (t * kVTile), x);
+          __syncthreads();
+        }
+        row_sum();
+        store_tile(x, t);
       }
+      store_sums();
+      return;
     }
-    __syncthreads();
-    if (wk == 1) return;
-    const float m1 = smerge[2 * row], l1 = smerge[2 * row + 1];
-    const float mn = fmaxf(m, m1), ref = mn == -INFINITY ? 0.0f : mn;
-    const float f0 = __builtin_amdgcn_exp2f(m - ref), f1 = __builtin_amdgcn_exp2f(m1 - ref);
-    m = mn;
-    l = l * f0 + l1 * f1;
-#pragma unroll
-    for (int t = 0; t < OT; ++t)
-#pragma unroll
-      for (int r = 0; r < SR; ++r)
-        o[t][r] = o[t][r] * f0 + so[(t * SR + r) * kWave + lane] * f1;
   }
-  if (row >= it.rows) return;
-  if (it.splits > 1) {
-    const int64_t p = (static_cast<int64_t>(it.slot) * a.kv_heads + h) * C::MT + row;
-    float* po = a.part_o + p * D;
+  row_sum();
 #pragma unroll
-    for (int t = 0; t < OT; ++t)
-#pragma unroll
-      for (int r = 0; r < SR; r += 4)
-        *reinterpret_cast<f32x4*>(po + t * RW + r * 2 + 4 * hi_lane) =
-            f32x4{o[t][r], o[t][r + 1], o[t][r + 2], o[t][r + 3]};
-    if (hi_lane == 0) {
-      a.part_ml[p * 2] = m;
-      a.part_ml[p * 2 + 1] = l;
-    }
-    return;
-  }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  const int64_t out = static_cast<int64_t>(token) * a.heads + head;
-  T* po = static_cast<T*>(a.out) + out * D;
-#pragma unroll
-  for (int t = 0; t < OT; ++t)
-#pragma unroll
-    for (int r = 0; r < SR; r += 4) {
-      typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-      *reinterpret_cast<u32x2*>(po + t * RW + r * 2 + 4 * hi_lane) =
-          u32x2{pack2<T>(o[t][r] * inv, o[t][r + 1] * inv),
-                pack2<T>(o[t][r + 2] * inv, o[t][r + 3] * inv)};
-    }
-  if (a.lse && hi_lane == 0) a.lse[out] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+  for (int t = 0; t < OT; ++t) store_tile(o[t], t);
+  store_sums();
 }
 
 template <class C>
@@ -447,17 +553,22 @@ void launch_cfg(const AttendArgs& a, hipStream_t st) {
                      dim3(C::W * kWave), 0, st, a);
 }
 
-// Tiles of 16, 32, 64 and 128 rows.  Up to 32 rows one set of rows is shared by
-// two wavefronts that take half a unit each (one at head_dim 256, whose unit is
-// half as long for the same LDS); above that each wavefront has 32 rows.
+// Tiles of 16, 32, 64 and 128 rows.  Up to 64 rows the cache's bandwidth bounds
+// the kernel: short units, most of them under way.  128 rows are bound by the
+// matrix and vector units: units of 64 positions, half the barriers.  Rows of
+// head_dim 256 leave LDS for two buffers and registers for 16 query rows a
+// wavefront, 64 a tile.
 template <typename T, int D>
 hipError_t launch_rows_of(const AttendArgs& a, int mt, hipStream_t st) {
-  constexpr int KT = D == 256 ? 32 : 64, WK = D == 256 ? 1 : 2;
+  constexpr bool kBig = D == 256;
+  constexpr int NB = kBig ? 2 : 4, RW = kBig ? 16 : 32;
   switch (mt) {
-    case 16: launch_cfg<AttendCfg<T, D, 16, 1, WK, KT>>(a, st); break;
-    case 32: launch_cfg<AttendCfg<T, D, 32, 1, WK, KT>>(a, st); break;
-    case 64: launch_cfg<AttendCfg<T, D, 32, 2, 1, KT>>(a, st); break;
-    default: launch_cfg<AttendCfg<T, D, 32, 4, 1, KT>>(a, st); break;
+    case 16: launch_cfg<AttendCfg<T, D, 16, 1, 32, NB>>(a, st); break;
+    case 32: launch_cfg<AttendCfg<T, D, RW, 32 / RW, 32, NB>>(a, st); break;
+    case 64: launch_cfg<AttendCfg<T, D, RW, 64 / RW, 32, NB>>(a, st); break;
+    default:
+      if constexpr (!kBig) launch_cfg<AttendCfg<T, D, 32, 4, 64, 2>>(a, st);
+      else return hipErrorInvalidValue;
   }
   return hipGetLastError();
 }

@@ -210,59 +210,80 @@ __global__ __launch_bounds__(kRowWaves * kWave) void attend_rows_kernel(AttendAr
 
 // Joins the splits of the tiles that were split: out = sum_s 2^(m_s - M) O_s /
 // sum_s 2^(m_s - M) l_s.  One workgroup per slot and key head; the slots of a
-// tile share its rows, and the wavefronts share a row's splits, which are
-// added in a fixed order.
+// tile share its rows.  A row is taken by head_dim / 4 threads, 4 elements
+// each; where there are fewer rows than such groups, several groups share a
+// row's splits and add up in a fixed order.
 template <typename T>
 __global__ __launch_bounds__(kRowWaves * kWave) void attend_join_kernel(AttendArgs a, int mt) {
-  __shared__ float so[kRowWaves][kMaxHeadDim];
-  __shared__ float sl[kRowWaves], sm[kRowWaves];
-  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  constexpr int NT = kRowWaves * kWave;
+  typedef float f4 __attribute__((ext_vector_type(4)));
+  __shared__ f4 so[NT];
+  __shared__ float sm[NT], sl[NT];
+  const int tid = threadIdx.x;
   const int slot = blockIdx.x / a.kv_heads, h = blockIdx.x - slot * a.kv_heads;
   const SlotInfo s = a.info[slot];
   if (slot >= *a.slot_count) return;
-  const int first = slot - s.split;
+  const int mine = s.split < s.rows ? (s.rows - s.split - 1) / s.splits + 1 : 0;
+  if (mine == 0) return;
+  const int lanes = a.D / 4, groups = NT / lanes;
+  const int parts = mine >= groups ? 1 : min(groups / mine, s.splits);
+  const int side = groups / parts;            // rows taken at a time
+  const int g = tid / lanes, d = (tid - g * lanes) * 4;
+  const int part = g % parts;
   const int64_t step = static_cast<int64_t>(a.kv_heads) * mt;
-  for (int r = s.split; r < s.rows; r += s.splits) {
-    const int64_t p0 = (static_cast<int64_t>(first) * a.kv_heads + h) * mt + r;
-    float mx = -INFINITY;
-    for (int i = tid; i < s.splits; i += kRowWaves * kWave)
-      mx = fmaxf(mx, a.part_ml[(p0 + i * step) * 2]);
-    mx = wave_max(mx);
-    __syncthreads();   // sm, sl and so of the row before are read
-    if (lane == 0) sm[wave] = mx;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kRowWaves; ++w) mx = fmaxf(mx, sm[w]);
-    const float ref = mx == -INFINITY ? 0.0f : mx;
-    float o[4] = {0.0f, 0.0f, 0.0f, 0.0f}, l = 0.0f;
+  const int64_t p00 = (static_cast<int64_t>(slot - s.split) * a.kv_heads + h) * mt;
+  // parts > 1 takes every row at once (side >= mine), so its barriers are met by all
+  for (int i = g / parts; i < mine || parts > 1; i += side) {
+    const bool in = i < mine && g < side * parts;
+    const int r = s.split + i * s.splits;
+    float mx = -INFINITY, l = 0.0f;
+    f4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (in) {
+      const float* ml = a.part_ml + (p00 + r) * 2;
+      const float* po = a.part_o + (p00 + r) * a.D + d;
 #pragma unroll 4
-    for (int i = wave; i < s.splits; i += kRowWaves) {
-      const int64_t p = p0 + i * step;
-      const float f = __builtin_amdgcn_exp2f(a.part_ml[p * 2] - ref);
-      l = fmaf(a.part_ml[p * 2 + 1], f, l);
-      const float* po = a.part_o + p * a.D;
+      for (int t = part; t < s.splits; t += parts) mx = fmaxf(mx, ml[t * step * 2]);
+      const float ref = mx == -INFINITY ? 0.0f : mx;
+#pragma unroll 4
+      for (int t = part; t < s.splits; t += parts) {
+        const float f = __builtin_amdgcn_exp2f(ml[t * step * 2] - ref);
+        l = fmaf(ml[t * step * 2 + 1], f, l);
+        const f4 x = *reinterpret_cast<const f4*>(po + t * step * a.D);
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (lane + j * kWave < a.D) o[j] = fmaf(po[lane + j * kWave], f, o[j]);
+        for (int e = 0; e < 4; ++e) o[e] = fmaf(x[e], f, o[e]);
+      }
     }
+    if (parts > 1) {
+      so[tid] = o;
+      sm[tid] = mx;
+      sl[tid] = l;
+      __syncthreads();
+      if (!in || part != 0) return;
+      for (int t = 1; t < parts; ++t) mx = fmaxf(mx, sm[tid + t * lanes]);
+      const float ref = mx == -INFINITY ? 0.0f : mx;
+      l = 0.0f;
+      o = f4{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int t = 0; t < parts; ++t) {
+        const float f = __builtin_amdgcn_exp2f(sm[tid + t * lanes] - ref);
+        l = fmaf(sl[tid + t * lanes], f, l);
+        const f4 x = so[tid + t * lanes];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (lane + j * kWave < a.D) so[wave][lane + j * kWave] = o[j];
-    if (lane == 0) sl[wave] = l;
-    __syncthreads();
-    float lw = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kRowWaves; ++w) lw += sl[w];
-    int token, head;
-    attend_row(a, s.token0, s.row0 + r, h, token, head);
-    const int64_t at = static_cast<int64_t>(token) * a.heads + head;
-    if (tid < a.D) {
-      float ow = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kRowWaves; ++w) ow += so[w][tid];
-      static_cast<T*>(a.out)[at * a.D + tid] = Elem<T>::store(lw == 0.0f ? 0.0f : ow / lw);
+        for (int e = 0; e < 4; ++e) o[e] = fmaf(x[e], f, o[e]);
+      }
     }
-    if (a.lse && tid == 0) a.lse[at] = lw == 0.0f ? -INFINITY : (ref + log2f(lw)) * kLn2;
+    if (in) {
+      int token, head;
+      attend_row(a, s.token0, s.row0 + r, h, token, head);
+      const int64_t at = static_cast<int64_t>(token) * a.heads + head;
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      typedef T t4 __attribute__((ext_vector_type(4)));
+      t4 y;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] = Elem<T>::store(o[e] * inv);
+      *reinterpret_cast<t4*>(static_cast<T*>(a.out) + at * a.D + d) = y;
+      if (a.lse && d == 0) a.lse[at] = l == 0.0f ? -INFINITY : (mx + log2f(l)) * kLn2;
+    }
+    if (parts > 1) return;
   }
 }
 

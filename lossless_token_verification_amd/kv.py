@@ -7,8 +7,11 @@ their device; every call is asynchronous.
 """
 
 import ctypes
+import sys
 
 import torch
+
+_pkg = sys.modules[__package__]      # the package, whose library() is the loaded build
 
 SV_DTYPE_F16 = 2
 MAX_HEAD_DIM = 256
@@ -55,27 +58,28 @@ def set_signatures(lib):
                                        ctypes.c_size_t, P]
 
 
-def _sv():
-    import lossless_token_verification_amd as sv
-    return sv
-
-
 def _call(fn, device, *args):
     """Calls an entry point on torch's current stream of ``device``, with that
     device current (the null stream belongs to the current device)."""
-    if not device.type == "cuda":
-        raise ValueError("tensors must be on a GPU")
-    if device.index is not None and device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    index = device.index
+    if torch._C._cuda_getDevice() == index:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
-        status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+        with torch.cuda.device(device):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if status:
-        _sv()._check(status)
+        _pkg._check(status)
+
+
+def _gpu(t):
+    """The device of a GPU tensor."""
+    if not t.is_cuda:
+        raise ValueError("tensors must be on a GPU")
+    return t.device
 
 
 def _tensor(t, name, dtype, shape, device):
-    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
         raise ValueError(f"{name} must be a contiguous {str(dtype)[6:]} tensor of shape "
                          f"{list(shape)} on {device}, got {str(t.dtype)[6:]} {list(t.shape)} on "
                          f"{t.device}")
@@ -126,8 +130,8 @@ def kv_blocktable_extend(block_table, seq_lens, num_new, free_blocks, free_count
     rows of the packed token arrays, at least the sum of num_new.  ``out``: a
     dict of an earlier call of the same shape, whose tensors are reused; its
     new_lens may be ``seq_lens`` and its free_left ``free_count``."""
-    lib = _sv().library()
-    dev, i32 = block_table.device, torch.int32
+    lib = _pkg.library()
+    dev, i32 = _gpu(block_table), torch.int32
     B, width = block_table.shape
     T = int(max_tokens)
     if T < 0:
@@ -168,10 +172,10 @@ def kv_cache_append(k, v, slot_map, k_cache, v_cache):
     rows allowed) to their slots of the caches [num_blocks, kv_heads, block_size,
     head_dim] in place.  ``slot_map`` [T] int64: negative or out-of-cache slots
     skip their row; the others must differ.  Float32, bfloat16 or float16."""
-    lib = _sv().library()
-    dev = k.device
+    lib = _pkg.library()
     if k.dtype not in _CODES:
         raise TypeError(f"k must be float32, bfloat16 or float16, got {k.dtype}")
+    dev = _gpu(k)
     nb, kv, bs, dim, block_stride = _caches(k_cache, v_cache, k.dtype, dev)
     if k.dim() != 3 or k.shape[1:] != (kv, dim) or v.shape != k.shape or v.dtype != k.dtype or \
             v.device != dev:
@@ -200,7 +204,7 @@ def kv_paged_attention_workspace_bytes(q, k_cache, v_cache, block_table, *, slid
                                        max_new=0):
     """Workspace bytes of ``kv_paged_attention`` on tensors of these shapes."""
     desc = _attention_desc(q, k_cache, v_cache, block_table, None, sliding_window, max_new)
-    return int(_sv().library().kv_paged_attention_workspace_bytes(ctypes.byref(desc)))
+    return int(_pkg.library().kv_paged_attention_workspace_bytes(ctypes.byref(desc)))
 
 
 def kv_paged_attention(q, k_cache, v_cache, block_table, seq_lens, cu_tokens, *, scale=None,
@@ -218,9 +222,9 @@ def kv_paged_attention(q, k_cache, v_cache, block_table, seq_lens, cu_tokens, *,
     [T, heads] float32 or None, workspace).  ``out``: a dict of an earlier call of
     the same shape, whose tensors are reused.  Rows of no sequence are left as
     they were."""
-    lib = _sv().library()
-    dev = q.device
+    lib = _pkg.library()
     desc = _attention_desc(q, k_cache, v_cache, block_table, scale, sliding_window, max_new)
+    dev = _gpu(q)
     B, T, heads, dim = desc.batch, desc.tokens, desc.heads, desc.head_dim
     pt = _tensor(block_table, "block_table", torch.int32, (B, desc.max_blocks), dev)
     pl = _tensor(seq_lens, "seq_lens", torch.int32, (B,), dev)
