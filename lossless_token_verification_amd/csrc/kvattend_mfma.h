@@ -73,6 +73,24 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{x, y}), t2));
 }
 
+// Maximum over the lane pairs N apart (16 or 32), by lane swaps on the vector
+// unit: the two results of swapping a value with itself hold, in every lane,
+// the pair's two values.
+template <int N>
+__device__ __forceinline__ float max_across(float x) {
+  const uint32_t w = __float_as_uint(x);
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  u32x2 p;
+  if constexpr (N == 32) {
+    const auto q = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+    p = u32x2{q[0], q[1]};
+  } else {
+    const auto q = __builtin_amdgcn_permlane16_swap(w, w, false, false);
+    p = u32x2{q[0], q[1]};
+  }
+  return fmaxf(__uint_as_float(p.x), __uint_as_float(p.y));
+}
+
 // LDS vector permutation of row r (D / 8 vectors a row; 256 bytes of LDS span
 // all banks: two rows at D = 64): vector v of row r lies at v ^ swz(r).  K: the
 // 16 consecutive rows an operand read takes at one vector fall on 16 different
@@ -149,7 +167,7 @@ __device__ __forceinline__ void wait_loads() {
 // registers and forms the products in them (given more, it moves every
 // accumulator through the other half of the file in each unit).
 template <class C>
-__global__ __launch_bounds__(4 * kWave) __attribute__((amdgpu_waves_per_eu(2))) void
+__global__ __launch_bounds__(4 * kWave) __attribute__((amdgpu_waves_per_eu(C::D == 64 ? 3 : 2))) void
 attend_mfma_kernel(AttendArgs a) {
   using T = typename C::T;
   constexpr int D = C::D, RW = C::RW, KT = C::KT, NB = C::NB, NV = C::NV, RPL = C::RPL;
@@ -224,7 +242,7 @@ attend_mfma_kernel(AttendArgs a) {
   auto load_unit = [&](int base, int64_t off, int from, uint16_t* sb) {
     constexpr int kUnroll = C::LOADS > 8 ? 4 : C::LOADS;
     int lk = lslot ^ swz_k<D>(lq), lv = lslot ^ swz_v<D>(lq);
-    if (D == 256) {   // many different lane parts: formed at each load
+    if (D != 128 || C::LOADS > 4) {   // registers are short: formed at each load
       lk = fresh(lk);
       lv = fresh(lv);
     }
@@ -330,8 +348,8 @@ attend_mfma_kernel(AttendArgs a) {
     for (int t = 0; t < ST; ++t)
 #pragma unroll
       for (int r = 0; r < SR; ++r) mx = fmaxf(mx, st[t][r]);
-    if (RW == 16) mx = fmaxf(mx, __shfl_xor(mx, 16, kWave));
-    mx = fmaxf(mx, __shfl_xor(mx, 32, kWave));
+    if (RW == 16) mx = max_across<16>(mx);
+    mx = max_across<32>(mx);
     const bool move = mx * c > m + kSlack;      // m = -inf: any score moves it
     if (__any(move)) {
       const float mn = move ? mx * c : m;
@@ -542,9 +560,42 @@ attend_mfma_kernel(AttendArgs a) {
     }
   }
   row_sum();
-#pragma unroll
-  for (int t = 0; t < OT; ++t) store_tile(o[t], t);
   store_sums();
+  if (it.splits > 1) {
+#pragma unroll
+    for (int t = 0; t < OT; ++t) store_tile(o[t], t);
+    return;
+  }
+  // whole output rows: turned in LDS (each wavefront its rows, permuted as K's),
+  // then 16 bytes a lane (8 bytes a lane straight from the registers touch every
+  // row in each store: 1024-token prompts 233 against 219 us)
+  static_assert(C::MT <= 2 * KT, "the rows fit the first buffer");
+  char* const turned = reinterpret_cast<char*>(sb0) + wave * RW * D * 2;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const int mine = lane & (RW - 1);
+#pragma unroll
+  for (int t = 0; t < OT; ++t)
+#pragma unroll
+    for (int r = 0; r < SR; r += 4) {
+      typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+      const int e = t * RW + r * 2 + 4 * hi_lane;     // element of the row
+      *reinterpret_cast<u32x2*>(turned + mine * (D * 2) + (((e >> 3) ^ swz_k<D>(mine)) << 4) +
+                                (e & 4) * 2) =
+          u32x2{pack2<T>(o[t][r] * inv, o[t][r + 1] * inv),
+                pack2<T>(o[t][r + 2] * inv, o[t][r + 3] * inv)};
+    }
+#pragma unroll
+  for (int i = 0; i < RW / RPL; ++i) {
+    const int r = i * RPL + lq;
+    const u32x4 w = *reinterpret_cast<const u32x4*>(turned + r * (D * 2) +
+                                                    ((lslot ^ swz_k<D>(r)) << 4));
+    if (wave * RW + r < it.rows) {
+      int token, head;
+      attend_row(a, it.token0, it.row0 + wave * RW + r, h, token, head);
+      T* po = static_cast<T*>(a.out) + (static_cast<int64_t>(token) * a.heads + head) * D;
+      reinterpret_cast<u32x4*>(po)[lslot] = w;
+    }
+  }
 }
 
 template <class C>
