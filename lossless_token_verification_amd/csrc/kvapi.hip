@@ -95,9 +95,10 @@ size_t pad256(size_t n) { return (n + 255) / 256 * 256; }
 // with the smallest tile that takes the rows of one sequence and key head
 // (rows: the caller's max_new, or the batch's mean, times the heads of a group).
 // wgs: items to aim at where keys are split, one for each workgroup the chip
-// holds.  A split costs a row 8 bytes of partial result per element, written
-// and read, a position 4 of cache: at 16 positions or more per row that stays
-// below an eighth.
+// holds.  min_units: a split costs a row 8 bytes of partial result per element,
+// written and read, a position 4 of cache; 4 positions per row and 64 at least
+// measured best where splits are that short, on a chip that is not full (9 rows
+// x 4 heads over 4000 positions: 26 us with 16 positions per row, 17 with 4).
 sv::AttendShape attend_shape(const spec_kv_attention_desc& d) {
   sv::AttendShape s{};
   const int D = d.head_dim;
@@ -108,8 +109,8 @@ sv::AttendShape attend_shape(const spec_kv_attention_desc& d) {
     const int64_t rows = n * (d.heads / d.kv_heads);
     s.mt = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 || D == 256 ? 64 : 128;
     s.kt = s.mt == 128 ? 64 : 32;
-    s.wgs = 512;
-    s.min_units = static_cast<int32_t>(std::max<int64_t>(64, 16 * std::min<int64_t>(rows, s.mt)) /
+    s.wgs = D == 64 ? (s.mt == 128 ? 768 : 1024) : 512;
+    s.min_units = static_cast<int32_t>(std::max<int64_t>(64, 4 * std::min<int64_t>(rows, s.mt)) /
                                        s.kt);
   } else {
     s.mt = D <= 64 ? sv::kRowsMT64 : D <= 128 ? sv::kRowsMT128 : sv::kRowsMT256;

@@ -57,6 +57,7 @@ template <int WAVES>
 struct AttendPlanShared {
   uint64_t sum[2][WAVES];
   uint64_t cls[kLengthClasses];
+  uint64_t items[WAVES];
   int32_t longest[WAVES];
   AttendItem item;
   int32_t found;
@@ -68,10 +69,12 @@ struct AttendPlanShared {
 // A sequence's keys are cut into splits of about S units, where S is what
 // spreads the call's units evenly over want_items workgroups and at least
 // min_units: with many tiles nothing is split, with few rows the key axis
-// fills the chip.  sum tiles * ceil(units / S) <= want_items where that leaves
-// room beside one split a tile (one workgroup too many of equal ones costs a
-// whole round: 461 against 322 us at B = 4, 110k positions), and never more
-// than want_items + tiles, which bounds the launch; the sequences that are
+// fills the chip: units / want_items if the splits then round up to want_items
+// at most (one workgroup too many of equal ones costs a whole round: 461 against
+// 322 us at B = 4, 110k positions), else units / (want_items - tiles), which
+// sum tiles * ceil(units / S) <= want_items follows from, or units /
+// (want_items / 2) where there is no such room.  There are never more than
+// want_items + tiles items, which bounds the launch; the sequences that are
 // split have units > S, so they use at most 2 want_items partial slots.  Items are numbered from the longest class of splits to the
 // shortest, so that the last workgroups to start are the short ones (B = 256,
 // 512 to 4096 positions: 474 -> 437 us).  Every workgroup makes these sums
@@ -117,12 +120,35 @@ __device__ __forceinline__ bool attend_find(const AttendArgs& a, int x, bool cou
   }
   int S = INT32_MAX;
   if (a.max_slots > 0) {
+    // a little over units / n, at least it
+    auto share = [&](int n) -> int {
+      const float f = static_cast<float>(units) * 1.0001f / static_cast<float>(n);
+      return max(a.min_units, f < 1e9f ? static_cast<int>(f) + 1 : INT32_MAX);
+    };
     const int64_t room = static_cast<int64_t>(a.want_items) - static_cast<int64_t>(tiles);
     const int over = max(static_cast<int>(max(room, static_cast<int64_t>(0))),
                          (a.want_items + 1) / 2);
-    // a little over units / over, at least it
-    const float share = static_cast<float>(units) * 1.0001f / static_cast<float>(over);
-    S = max(a.min_units, share < 1e9f ? static_cast<int>(share) + 1 : INT32_MAX);
+    S = share(a.want_items);      // if the splits round up to few enough items
+    uint64_t items = tiles;
+    if (tiles <= static_cast<uint64_t>(a.want_items)) {
+      items = 0;
+      for (int b = tid; b < a.B; b += NT) {
+        const AttendSeq s = attend_seq<MT, KT>(a, b);
+        items += static_cast<uint64_t>(s.tiles) *
+                 max((static_cast<uint32_t>(s.units) + S - 1) / S, 1u);
+      }
+#pragma unroll
+      for (int o = 32; o > 0; o >>= 1)
+        items += __shfl_xor(static_cast<unsigned long long>(items), o, kWave);
+      if (WAVES > 1) {
+        if (lane == 0) sh.items[wave] = items;
+        __syncthreads();
+        items = 0;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) items += sh.items[w];
+      }
+    }
+    if (items > static_cast<uint64_t>(a.want_items)) S = share(over);
   }
   // splits of a sequence, their length's class and its (items << 32) + slots
   const int top = min(longest, S);

@@ -13,7 +13,9 @@
 // The bytes are few (12 per token, a handful per sequence), so what counts is
 // the latency of the launches: one workgroup makes the prefix sums and, up to
 // kFusedTokens tokens, fills the token arrays itself; beyond that a second
-// launch spreads the fill over the chip.
+// launch spreads the fill over the chip.  A batch of one thread per sequence
+// keeps the sums' results in LDS for the fill and scans by lane moves on the
+// vector unit.
 #include "kv_args.h"
 
 namespace sv {
@@ -53,16 +55,114 @@ __device__ __forceinline__ int64_t ceil_blocks(int64_t n, const FastDiv& bs) {
   return n > 0 ? fast_div(static_cast<int>(n - 1), bs) + 1 : 0;
 }
 
+// Inclusive prefix sum over a wavefront by lane moves: shifts within rows of 16
+// lanes, then the last lane of a row, or of both, added to the rows after it.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t scan_step(uint32_t x) {
+  return x + __builtin_amdgcn_update_dpp(0, x, CTRL, ROWS, 0xf, false);
+}
+__device__ __forceinline__ uint32_t wave_scan(uint32_t x) {
+  x = scan_step<0x111, 0xf>(x);
+  x = scan_step<0x112, 0xf>(x);
+  x = scan_step<0x114, 0xf>(x);
+  x = scan_step<0x118, 0xf>(x);
+  x = scan_step<0x142, 0xa>(x);
+  return scan_step<0x143, 0xc>(x);
+}
+
+// Exclusive prefix sums of two values over the workgroup (sums below 2^32); the
+// totals in *ta and *tb.  scratch: two values per wavefront, not used since the
+// last barrier.
+__device__ __forceinline__ void block_scan2(uint32_t& x, uint32_t& y, uint32_t* scratch,
+                                            uint32_t* ta, uint32_t* tb) {
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  const int waves = blockDim.x / kWave;
+  const uint32_t a = wave_scan(x), b = wave_scan(y);
+  if (lane == kWave - 1) {
+    scratch[2 * wave] = a;
+    scratch[2 * wave + 1] = b;
+  }
+  __syncthreads();
+  uint32_t before_a = 0, before_b = 0, all_a = 0, all_b = 0;
+  for (int w = 0; w < waves; ++w) {
+    const uint32_t p = scratch[2 * w], q = scratch[2 * w + 1];
+    if (w < wave) {
+      before_a += p;
+      before_b += q;
+    }
+    all_a += p;
+    all_b += q;
+  }
+  *ta = all_a;
+  *tb = all_b;
+  x = before_a + a - x;
+  y = before_b + b - y;
+}
+
+// Rows [lo, hi) of the token arrays, all of the m sequences from c on, whose
+// first rows (m + 1 of them), lengths before (-1: not served) and stack tops
+// are in LDS.  Four rows a thread at a time: their lookups before their stores.
+__device__ __forceinline__ void fill_chunk(const ExtendArgs& a, int c, int m, int lo, int hi,
+                                           const int32_t* s_cu, const int32_t* s_len,
+                                           const int64_t* s_off) {
+  constexpr int kSide = 4;
+  const int tid = threadIdx.x, nt = blockDim.x;
+  const int first = s_cu[0], all = s_cu[m] - first;
+  const float rate = all > 0 ? static_cast<float>(m) / static_cast<float>(all) : 0.0f;
+  for (int t0 = lo + tid; t0 < hi; t0 += kSide * nt) {
+    int pos[kSide], row[kSide], id[kSide];
+    int32_t* fresh_entry[kSide];
+#pragma unroll
+    for (int i = 0; i < kSide; ++i) {
+      const int t = t0 + i * nt;
+      pos[i] = -1;
+      fresh_entry[i] = nullptr;
+      if (t >= hi) continue;
+      // the last sequence that starts at or before t: where equal shares would
+      // have it, or by bisection
+      int l = min(static_cast<int>(static_cast<float>(t - first) * rate), m - 1);
+      if (s_cu[l] > t || s_cu[l + 1] <= t) {
+        l = 0;
+        for (int r = m; r - l > 1;) {
+          const int mid = (l + r) >> 1;
+          if (s_cu[mid] <= t) l = mid; else r = mid;
+        }
+      }
+      const int len = s_len[l];
+      if (len < 0) continue;
+      pos[i] = len + (t - s_cu[l]);
+      const int lb = fast_div(pos[i], a.bs);
+      row[i] = pos[i] - lb * a.block_size;
+      const int64_t fresh = lb - ceil_blocks(len, a.bs);   // index among the blocks just taken
+      int32_t* entry = a.table + static_cast<int64_t>(c + l) * a.max_blocks + lb;
+      id[i] = fresh >= 0 ? a.free_blocks[s_off[l] - fresh] : *entry;
+      if (fresh >= 0 && row[i] == 0) fresh_entry[i] = entry;
+    }
+#pragma unroll
+    for (int i = 0; i < kSide; ++i) {
+      const int t = t0 + i * nt;
+      if (t >= hi) break;
+      if (fresh_entry[i]) *fresh_entry[i] = id[i];
+      a.slots[t] = pos[i] < 0 ? -1 : static_cast<int64_t>(id[i]) * a.block_size + row[i];
+      if (a.positions) a.positions[t] = pos[i];
+    }
+  }
+}
+
+// Rows [t0, t1) behind the last token.
+__device__ __forceinline__ void fill_rest(const ExtendArgs& a, int t0, int t1) {
+  for (int t = t0 + threadIdx.x; t < t1; t += blockDim.x) {
+    a.slots[t] = -1;
+    if (a.positions) a.positions[t] = -1;
+  }
+}
+
 // Fills rows [t0, t1) of the token arrays from the plan's outputs (cu,
 // new_lens, num_taken, free_left), a chunk of blockDim.x sequences at a time.
 __device__ void fill_tokens(const ExtendArgs& a, int t0, int t1, int64_t* scratch, int32_t* s_cu,
                             int32_t* s_len, int64_t* s_off) {
   const int tid = threadIdx.x, nt = blockDim.x;
-  const int used = a.cu[a.B];
-  for (int t = max(t0, used) + tid; t < t1; t += nt) {
-    a.slots[t] = -1;
-    if (a.positions) a.positions[t] = -1;
-  }
+  fill_rest(a, max(t0, a.cu[a.B]), t1);
   // ids in the stack before any was taken: what is left and what was taken
   int64_t taken_all = 0;
   if (a.B > nt)
@@ -88,33 +188,7 @@ __device__ void fill_tokens(const ExtendArgs& a, int t0, int t1, int64_t* scratc
       s_off[tid] = top - 1 - off;
     }
     __syncthreads();
-    const int lo = max(t0, s_cu[0]), hi = min(t1, s_cu[m]);
-    for (int t = lo + tid; t < hi; t += nt) {
-      int l = 0, r = m;   // the last sequence of the chunk that starts at or before t
-      while (r - l > 1) {
-        const int mid = (l + r) >> 1;
-        if (s_cu[mid] <= t) l = mid; else r = mid;
-      }
-      const int len = s_len[l];
-      if (len < 0) {
-        a.slots[t] = -1;
-        if (a.positions) a.positions[t] = -1;
-        continue;
-      }
-      const int pos = len + (t - s_cu[l]);
-      const int lb = fast_div(pos, a.bs), row = pos - lb * a.block_size;
-      const int64_t fresh = lb - ceil_blocks(len, a.bs);   // index among the blocks just taken
-      int32_t* entry = a.table + static_cast<int64_t>(c + l) * a.max_blocks + lb;
-      int32_t id;
-      if (fresh >= 0) {
-        id = a.free_blocks[s_off[l] - fresh];
-        if (row == 0) *entry = id;
-      } else {
-        id = *entry;
-      }
-      a.slots[t] = static_cast<int64_t>(id) * a.block_size + row;
-      if (a.positions) a.positions[t] = pos;
-    }
+    fill_chunk(a, c, m, max(t0, s_cu[0]), min(t1, s_cu[m]), s_cu, s_len, s_off);
     __syncthreads();
   }
 }
@@ -124,7 +198,61 @@ struct FillShared {
   int64_t off[kScanThreads];
   int32_t cu[kScanThreads + 1];
   int32_t len[kScanThreads];
+  int32_t given;   // blocks handed out
 };
+
+// One thread per sequence (B <= blockDim, B * (T + 1) < 2^32).
+__global__ __launch_bounds__(kScanThreads) void extend_small_kernel(ExtendArgs a, int fused) {
+  __shared__ FillShared sh;
+  __shared__ uint32_t scratch[2][2 * kScanThreads / kWave];
+  const int b = threadIdx.x;
+  const bool in = b < a.B;
+  const int64_t L = in ? a.lens[b] : 0, n = in ? a.num_new[b] : 0;
+  const int m = in && a.freed ? min(max(a.num_freed[b], 0), a.max_freed) : 0;
+  const int count = min(max(a.free_count[0], 0), a.free_capacity);
+  if (b == 0) sh.given = 0;
+  const uint32_t want = static_cast<uint32_t>(
+      min(max(n, static_cast<int64_t>(0)), static_cast<int64_t>(a.T) + 1));
+  uint32_t at = m, first = want, pushed, rows;
+  block_scan2(at, first, scratch[0], &pushed, &rows);
+  const int64_t top = min(static_cast<int64_t>(count) + pushed,
+                          static_cast<int64_t>(a.free_capacity));
+  for (int i = 0; i < m && static_cast<int64_t>(count) + at + i < a.free_capacity; ++i)
+    a.free_blocks[static_cast<int64_t>(count) + at + i] =
+        a.freed[static_cast<int64_t>(b) * a.max_freed + i];
+  const int64_t cap = min(static_cast<int64_t>(a.max_blocks) * a.block_size,
+                          static_cast<int64_t>(INT32_MAX));
+  const bool good = n >= 0 && L >= 0 && L + n <= cap &&
+                    static_cast<int64_t>(first) + want <= a.T;
+  const uint32_t need =
+      good ? static_cast<uint32_t>(ceil_blocks(L + n, a.bs) - ceil_blocks(L, a.bs)) : 0;
+  uint32_t off = need, none = 0, unused_total, all_need;
+  block_scan2(off, none, scratch[1], &all_need, &unused_total);
+  const bool served = good && (need == 0 || static_cast<int64_t>(off) + need <= top);
+  if (in) {
+    const int lo = static_cast<int>(min(first, static_cast<uint32_t>(a.T)));
+    a.new_lens[b] = static_cast<int32_t>(served ? L + n : L);
+    a.num_taken[b] = served ? static_cast<int32_t>(need) : good ? -2 : -1;
+    a.cu[b] = lo;
+    sh.cu[b] = lo;
+    sh.len[b] = served ? static_cast<int32_t>(L) : -1;
+    sh.off[b] = top - 1 - off;
+    // the served sequences that need blocks are the first ones: the last of them
+    // knows how many were taken
+    if (served && need > 0 && static_cast<int64_t>(off) + need <= top)
+      atomicMax(&sh.given, static_cast<int32_t>(off + need));
+  }
+  const int used = static_cast<int>(min(rows, static_cast<uint32_t>(a.T)));
+  if (b == 0) {
+    a.cu[a.B] = used;
+    sh.cu[a.B] = used;
+  }
+  __syncthreads();
+  if (b == 0) a.free_left[0] = static_cast<int32_t>(top - sh.given);
+  if (!fused) return;
+  fill_rest(a, used, a.T);
+  if (a.B > 0) fill_chunk(a, 0, a.B, 0, used, sh.cu, sh.len, sh.off);
+}
 
 __global__ __launch_bounds__(kScanThreads) void extend_kernel(ExtendArgs a, int fused) {
   __shared__ FillShared sh;
@@ -187,7 +315,12 @@ hipError_t launch_extend(const ExtendArgs& a, hipStream_t st) {
   const int work = max(a.B, fused ? min(a.T, kScanThreads) : 0);
   const unsigned threads = static_cast<unsigned>(
       min(kScanThreads, max(kWave, (work + kWave - 1) / kWave * kWave)));
-  hipLaunchKernelGGL(extend_kernel, dim3(1), dim3(threads), 0, st, a, fused);
+  const bool small = a.B <= static_cast<int>(threads) &&
+                     static_cast<int64_t>(a.B) * (static_cast<int64_t>(a.T) + 1) < UINT32_MAX;
+  if (small)
+    hipLaunchKernelGGL(extend_small_kernel, dim3(1), dim3(threads), 0, st, a, fused);
+  else
+    hipLaunchKernelGGL(extend_kernel, dim3(1), dim3(threads), 0, st, a, fused);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess || fused) return err;
   hipLaunchKernelGGL(fill_kernel, dim3((a.T + kFillTokens - 1) / kFillTokens), dim3(kFillThreads),
