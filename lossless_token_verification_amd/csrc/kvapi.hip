@@ -158,10 +158,11 @@ int32_t make_attend_plan(const spec_kv_attention_desc* d, AttendPlan* p) {
   const int64_t mt = p->shape.mt, kt = p->shape.kt;
   const int64_t tiles = d->tokens * group / mt + std::min(d->batch, d->tokens);
   const int64_t want = std::max<int64_t>(1, p->shape.wgs / d->kv_heads);
-  int64_t keys = cap;   // most positions the rows of a sequence see together
+  // Most units the rows of a sequence see together: from position 0 on, or, with
+  // a window, W + T - 1 positions from anywhere.
+  int64_t units = (cap + kt - 1) / kt;
   if (d->sliding_window > 0)
-    keys = std::min<int64_t>(keys, static_cast<int64_t>(d->sliding_window) + d->tokens);
-  const int64_t units = keys / kt + 2;
+    units = std::min(units, (static_cast<int64_t>(d->sliding_window) + d->tokens) / kt + 2);
   const int64_t splits = (units + p->shape.min_units - 1) / p->shape.min_units;
   const int64_t slots = splits > 1 ? std::min(2 * want, tiles * splits) : 0;
   const int64_t items = std::min(want + tiles, tiles * splits);

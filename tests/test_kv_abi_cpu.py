@@ -147,7 +147,7 @@ def test_attention_workspace(sv, kv):
     assert _attend(sv, kv, dict(ws=ctypes.c_void_p(0x1010)), **long) == 4
     assert _attend(sv, kv, ws_bytes=need - 1, **long) == 4
     # contexts of one split, and a window that keeps them so, need none
-    assert _ws(sv, kv, max_blocks=8) == 0
+    assert _ws(sv, kv, max_blocks=4) == 0
     assert _ws(sv, kv, sliding_window=16, **long) == 0
     # nothing to do: no launch, no pointers
     for kw in (dict(batch=0), dict(tokens=0)):
