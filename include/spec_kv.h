@@ -139,7 +139,8 @@ typedef struct {
   int64_t q_stride;       /* elements between q's token rows; 0 => heads * head_dim */
   int64_t block_stride;   /* elements between blocks of a cache; 0 =>
                              kv_heads * block_size * head_dim                     */
-  float scale;            /* of the scores, > 0 and finite (often head_dim^-0.5)  */
+  float scale;            /* of the scores, > 0, scale * log2(e) finite (often
+                             head_dim^-0.5)                                       */
   float reserved_f;       /* must be 0                                           */
 } spec_kv_attention_desc;
 
@@ -164,8 +165,9 @@ size_t kv_paged_attention_workspace_bytes(const spec_kv_attention_desc* desc);
  *               positions beyond the table
  *   seq_lens    [B] device int32 (with the new tokens)
  *   cu_tokens   [B+1] device int32, ascending within [0, T] (values outside are
- *               limited to it); rows before the first and behind the last
- *               sequence are left as they were
+ *               limited to it; where ranges overlap, which rows are written is
+ *               undefined); rows before the first and behind the last sequence
+ *               are left as they were
  *   out         [T, heads, head_dim] device
  *   lse         [T, heads] device float32 or NULL
  *   workspace   256-byte aligned, >= kv_paged_attention_workspace_bytes(desc);

@@ -49,7 +49,7 @@ struct AppendArgs {
   const void* src[2];        // k, v
   void* dst[2];              // k_cache, v_cache
   const int64_t* slots;
-  int32_t T, vec_bytes;      // bytes one thread moves: 16, or one element
+  int32_t T, vec_bytes;      // T * row_vecs < 2^31; bytes one thread moves: 16, or an element
   int32_t row_vecs;          // vectors of one token row (kv_heads * head_vecs)
   int32_t head_vecs;         // vectors of one head of a row
   int32_t num_slots, block_size;
@@ -82,6 +82,7 @@ struct AttendArgs {
   int32_t min_units;    // fewest key units (of the kernel's KT keys) of a split
   int32_t max_slots;    // partial slots per key head in the workspace (0: never split)
   int32_t grid_items;   // launched (tile, split) items per key head
+  int64_t max_tiles;    // most tiles of token ranges that do not overlap
   struct SlotInfo* info;   // [max_slots]
   int32_t* slot_count;     // slots in use
   float* part_o;        // [max_slots * kv_heads, MT, D]

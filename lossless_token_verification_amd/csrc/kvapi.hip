@@ -46,6 +46,7 @@ int32_t check_ptr(const void* p, bool required, uintptr_t align, const char* nam
 constexpr int32_t kMaxHeads = 1 << 16;
 constexpr int32_t kMaxRowDim = 1 << 12;   // head_dim of a cache append
 constexpr int64_t kMaxStride = int64_t{1} << 40;
+constexpr int64_t kMaxWorkgroups = int64_t{1} << 24;
 
 int dtype_bytes(int dtype) { return dtype == SV_DTYPE_F32 ? 4 : 2; }
 
@@ -86,6 +87,7 @@ struct AttendPlan {
   sv::AttendShape shape{};
   int64_t q_stride = 0, block_stride = 0;
   int32_t cap = 0, want_items = 0, max_slots = 0, grid_items = 0;
+  int64_t max_tiles = 0;
   size_t info_bytes = 0, ml_bytes = 0, o_bytes = 0, ws_bytes = 0;
 };
 
@@ -141,8 +143,9 @@ int32_t make_attend_plan(const spec_kv_attention_desc* d, AttendPlan* p) {
     return fail(SV_ERR_INVALID_ARG, "heads is not a multiple of kv_heads");
   if (static_cast<int64_t>(d->tokens) * d->heads > INT32_MAX)
     return fail(SV_ERR_UNSUPPORTED, "tokens * heads >= 2^31");
-  if (!(d->scale > 0.0f) || !std::isfinite(d->scale))
-    return fail(SV_ERR_INVALID_ARG, "scale must be positive and finite");
+  // (the kernels hold scores in units of log2: scale * log2 e)
+  if (!(d->scale > 0.0f) || !std::isfinite(d->scale * sv::kLog2e))
+    return fail(SV_ERR_INVALID_ARG, "scale must be positive and scale * log2(e) finite");
   p->q_stride = d->q_stride;
   SV_TRY(check_stride(&p->q_stride, static_cast<int64_t>(d->heads) * d->head_dim, "q_stride"));
   const int es = dtype_bytes(d->dtype);
@@ -166,11 +169,13 @@ int32_t make_attend_plan(const spec_kv_attention_desc* d, AttendPlan* p) {
   const int64_t splits = (units + p->shape.min_units - 1) / p->shape.min_units;
   const int64_t slots = splits > 1 ? std::min(2 * want, tiles * splits) : 0;
   const int64_t items = std::min(want + tiles, tiles * splits);
-  if (items * d->kv_heads > INT32_MAX || slots * d->kv_heads > INT32_MAX)
+  // 256 threads an item: a launch takes fewer than 2^32
+  if (items * d->kv_heads >= kMaxWorkgroups || slots * d->kv_heads >= kMaxWorkgroups)
     return fail(SV_ERR_UNSUPPORTED, "batch too large for one call");
   p->want_items = static_cast<int32_t>(want);
   p->max_slots = static_cast<int32_t>(slots);
   p->grid_items = static_cast<int32_t>(items);
+  p->max_tiles = tiles;
   if (slots > 0) {
     const size_t rows = static_cast<size_t>(slots) * d->kv_heads * mt;
     p->info_bytes = pad256(static_cast<size_t>(slots) * sizeof(sv::SlotInfo));
@@ -265,16 +270,10 @@ int32_t kv_cache_append(const spec_kv_append_desc* desc, const void* k, const vo
                     aligned_to(k, 16) && aligned_to(v, 16) && aligned_to(k_cache, 16) &&
                     aligned_to(v_cache, 16);
   const int vb = wide ? 16 : es, per = vb / es;
-  if (d.tokens * (row / per) / 256 >= INT32_MAX)
-    return fail(SV_ERR_UNSUPPORTED, "too many rows for one call");
   if (!any || d.num_blocks == 0) return SV_OK;
   sv::AppendArgs a{};
-  a.src[0] = k;
-  a.src[1] = v;
   a.dst[0] = k_cache;
   a.dst[1] = v_cache;
-  a.slots = slot_map;
-  a.T = d.tokens;
   a.vec_bytes = vb;
   a.row_vecs = static_cast<int32_t>(row / per);
   a.head_vecs = d.head_dim / per;
@@ -286,8 +285,16 @@ int32_t kv_cache_append(const spec_kv_append_desc* desc, const void* k, const vo
   a.src_stride[0] = k_stride / per;
   a.src_stride[1] = v_stride / per;
   a.block_stride = block_stride / per;
-  const hipError_t err = sv::launch_append(a, static_cast<hipStream_t>(hip_stream));
-  if (err != hipSuccess) return device_error(err, "cache append launch");
+  // one launch, or as many as keep a launch's vectors below 2^31
+  const int64_t step = INT32_MAX / a.row_vecs;
+  for (int64_t t = 0; t < d.tokens; t += step) {
+    a.src[0] = static_cast<const char*>(k) + t * k_stride * es;
+    a.src[1] = static_cast<const char*>(v) + t * v_stride * es;
+    a.slots = slot_map + t;
+    a.T = static_cast<int32_t>(std::min<int64_t>(step, d.tokens - t));
+    const hipError_t err = sv::launch_append(a, static_cast<hipStream_t>(hip_stream));
+    if (err != hipSuccess) return device_error(err, "cache append launch");
+  }
   return SV_OK;
 }
 
@@ -351,6 +358,7 @@ int32_t kv_paged_attention(const spec_kv_attention_desc* desc, const void* q,
   a.min_units = p.shape.min_units;
   a.max_slots = p.max_slots;
   a.grid_items = p.grid_items;
+  a.max_tiles = p.max_tiles;
   if (p.ws_bytes > 0) {
     char* ws = static_cast<char*>(workspace);
     a.slot_count = reinterpret_cast<int32_t*>(ws);

@@ -10,11 +10,11 @@ namespace {
 constexpr int kAppendThreads = 256;
 
 template <typename V>
-__global__ __launch_bounds__(kAppendThreads) void append_kernel(AppendArgs a, int64_t total) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kAppendThreads + threadIdx.x;
+__global__ __launch_bounds__(kAppendThreads) void append_kernel(AppendArgs a, uint32_t total) {
+  const uint32_t i = blockIdx.x * kAppendThreads + threadIdx.x;
   if (i >= total) return;
-  const int t = static_cast<int>(i / a.row_vecs);
-  const int c = static_cast<int>(i - static_cast<int64_t>(t) * a.row_vecs);
+  const int t = fast_div(static_cast<int>(i), a.row);
+  const int c = static_cast<int>(i) - t * a.row_vecs;
   const int64_t slot = a.slots[t];
   if (slot < 0 || slot >= a.num_slots) return;
   const int h = fast_div(c, a.head), d = c - h * a.head_vecs;
@@ -31,8 +31,8 @@ __global__ __launch_bounds__(kAppendThreads) void append_kernel(AppendArgs a, in
 }  // namespace
 
 hipError_t launch_append(const AppendArgs& a, hipStream_t st) {
-  const int64_t total = static_cast<int64_t>(a.T) * a.row_vecs;
-  const dim3 grid(static_cast<unsigned>((total + kAppendThreads - 1) / kAppendThreads));
+  const uint32_t total = static_cast<uint32_t>(a.T) * a.row_vecs;
+  const dim3 grid((total + kAppendThreads - 1) / kAppendThreads);
   if (a.vec_bytes == 16)
     hipLaunchKernelGGL(append_kernel<u32x4>, grid, dim3(kAppendThreads), 0, st, a, total);
   else if (a.vec_bytes == 4)

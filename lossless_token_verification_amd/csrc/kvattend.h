@@ -24,6 +24,8 @@ struct AttendSeq {
 
 // A sequence's extent; every value read from the device arrays is limited to
 // what the descriptor allows, so that nothing out of range is ever addressed.
+// Token ranges that overlap (offsets that do not ascend) can have more tiles
+// than the launch and the workspace were sized for: attend_find then takes none.
 template <int MT, int KT>
 __device__ __forceinline__ AttendSeq attend_seq(const AttendArgs& a, int b) {
   AttendSeq s;
@@ -116,6 +118,10 @@ __device__ __forceinline__ bool attend_find(const AttendArgs& a, int x, bool cou
         tiles += sh.sum[1][w];
         longest = max(longest, sh.longest[w]);
       }
+    }
+    if (tiles > static_cast<uint64_t>(a.max_tiles)) {   // offsets that do not ascend
+      if (count_slots && tid == 0) *a.slot_count = 0;
+      return false;
     }
   }
   int S = INT32_MAX;

@@ -202,7 +202,7 @@ attend_mfma_kernel(AttendArgs a) {
     attend_row(a, it.token0, it.row0 + min(row, it.rows - 1), h, token, head);
     const int pos = it.pos0 + token - it.token0;
     const int key_last = min(pos, it.key_hi - 1);
-    const int key_first = a.window > 0 ? max(pos - a.window + 1, 0) : 0;
+    const int key_first = a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
     see_lo = key_last >= key_first ? key_first : INT32_MAX;
     see_span = key_last >= key_first ? key_last - key_first : 0;
     const T* qr = static_cast<const T*>(a.q) + token * a.q_stride + static_cast<int64_t>(head) * D;
@@ -212,8 +212,8 @@ attend_mfma_kernel(AttendArgs a) {
   }
   // positions every row of the tile may see: units inside need no mask
   const int all_hi = min(it.pos0 + fast_div(it.row0, a.grp), it.key_hi - 1);
-  const int all_lo =
-      a.window > 0 ? it.pos0 + fast_div(it.row0 + it.rows - 1, a.grp) - a.window + 1 : 0;
+  const int pos_last = it.pos0 + fast_div(it.row0 + it.rows - 1, a.grp);
+  const int all_lo = a.window > 0 && pos_last >= a.window ? pos_last - a.window + 1 : 0;
 
   const int32_t* table = a.table + static_cast<int64_t>(it.b) * a.max_blocks;
   const int64_t head_off = static_cast<int64_t>(h) * a.block_size;

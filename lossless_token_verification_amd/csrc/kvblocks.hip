@@ -201,7 +201,7 @@ struct FillShared {
   int32_t given;   // blocks handed out
 };
 
-// One thread per sequence (B <= blockDim, B * (T + 1) < 2^32).
+// One thread per sequence (B <= blockDim; B * (T + 1) and B * max_freed below 2^32).
 __global__ __launch_bounds__(kScanThreads) void extend_small_kernel(ExtendArgs a, int fused) {
   __shared__ FillShared sh;
   __shared__ uint32_t scratch[2][2 * kScanThreads / kWave];
@@ -316,7 +316,7 @@ hipError_t launch_extend(const ExtendArgs& a, hipStream_t st) {
   const unsigned threads = static_cast<unsigned>(
       min(kScanThreads, max(kWave, (work + kWave - 1) / kWave * kWave)));
   const bool small = a.B <= static_cast<int>(threads) &&
-                     static_cast<int64_t>(a.B) * (static_cast<int64_t>(a.T) + 1) < UINT32_MAX;
+                     static_cast<int64_t>(a.B) * (max(a.T, a.max_freed) + int64_t{1}) < UINT32_MAX;
   if (small)
     hipLaunchKernelGGL(extend_small_kernel, dim3(1), dim3(threads), 0, st, a, fused);
   else

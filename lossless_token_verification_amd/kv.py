@@ -86,6 +86,14 @@ def _tensor(t, name, dtype, shape, device):
     return t.data_ptr()
 
 
+def _i32(value, name):
+    """An argument of the C ABI's 32-bit type (ctypes would cut it to size)."""
+    value = int(value)
+    if not -0x80000000 <= value <= 0x7fffffff:
+        raise ValueError(f"{name} must be a 32-bit integer, got {value}")
+    return value
+
+
 def _caches(k_cache, v_cache, dtype, device):
     """(blocks, kv_heads, block_size, head_dim, block stride) of a cache pair."""
     if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
@@ -101,9 +109,12 @@ def _caches(k_cache, v_cache, dtype, device):
             raise ValueError(f"{name}: each block must be contiguous")
     if nb <= 1:
         return nb, kv, bs, dim, 0
-    if k_cache.stride(0) != v_cache.stride(0):
+    stride = k_cache.stride(0)
+    if stride != v_cache.stride(0):
         raise ValueError("k_cache and v_cache must have one block stride")
-    return nb, kv, bs, dim, k_cache.stride(0)
+    if stride < kv * bs * dim:                  # (an expanded cache has 0)
+        raise ValueError("the blocks of a cache must not overlap")
+    return _i32(nb, "num_blocks"), kv, bs, dim, stride
 
 
 def _row_stride(t, name):
@@ -113,7 +124,11 @@ def _row_stride(t, name):
     s = t.stride()
     if (dim > 1 and s[2] != 1) or (heads > 1 and s[1] != dim):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
-    return s[0] if T > 1 else 0
+    if T <= 1:
+        return 0
+    if s[0] < heads * dim:                      # (an expanded row has 0)
+        raise ValueError(f"{name}: the token rows must not overlap")
+    return s[0]
 
 
 def kv_blocktable_extend(block_table, seq_lens, num_new, free_blocks, free_count, block_size,
@@ -133,7 +148,7 @@ def kv_blocktable_extend(block_table, seq_lens, num_new, free_blocks, free_count
     lib = _pkg.library()
     dev, i32 = _gpu(block_table), torch.int32
     B, width = block_table.shape
-    T = int(max_tokens)
+    T = _i32(max_tokens, "max_tokens")
     if T < 0:
         raise ValueError("max_tokens must not be negative")
     p = (_tensor(block_table, "block_table", i32, (B, width), dev),
@@ -156,7 +171,7 @@ def kv_blocktable_extend(block_table, seq_lens, num_new, free_blocks, free_count
                    cu_tokens=torch.empty(B + 1, dtype=i32, device=dev),
                    slot_map=torch.empty(T, dtype=torch.int64, device=dev),
                    positions=torch.empty(T, dtype=i32, device=dev))
-    _call(lib.kv_blocktable_extend, dev, B, width, int(block_size), p[0], p[1], p[2], p[3],
+    _call(lib.kv_blocktable_extend, dev, B, width, _i32(block_size, "block_size"), p[0], p[1], p[2], p[3],
           free_blocks.numel(), pc, pf, max_freed, pn, T,
           _tensor(out["new_lens"], "out new_lens", i32, (B,), dev),
           _tensor(out["num_taken"], "out num_taken", i32, (B,), dev),
@@ -180,7 +195,7 @@ def kv_cache_append(k, v, slot_map, k_cache, v_cache):
     if k.dim() != 3 or k.shape[1:] != (kv, dim) or v.shape != k.shape or v.dtype != k.dtype or \
             v.device != dev:
         raise ValueError(f"k and v must be [T, {kv}, {dim}] of one dtype on one device")
-    T = k.shape[0]
+    T = _i32(k.shape[0], "T")
     desc = AppendDesc(T, kv, dim, bs, nb, _CODES[k.dtype], _row_stride(k, "k"),
                       _row_stride(v, "v"), block_stride)
     _call(lib.kv_cache_append, dev, ctypes.byref(desc), k.data_ptr(), v.data_ptr(),
@@ -195,8 +210,9 @@ def _attention_desc(q, k_cache, v_cache, block_table, scale, sliding_window, max
     if q.dim() != 3 or q.shape[2] != dim:
         raise ValueError(f"q must be [T, heads, {dim}]")
     B, width = block_table.shape
-    return AttentionDesc(B, q.shape[0], q.shape[1], kv, dim, bs, nb, width, _CODES[q.dtype],
-                         int(sliding_window), int(max_new), 0, _row_stride(q, "q"), block_stride,
+    return AttentionDesc(B, _i32(q.shape[0], "T"), q.shape[1], kv, dim, bs, nb, width,
+                         _CODES[q.dtype], _i32(sliding_window, "sliding_window"),
+                         _i32(max_new, "max_new"), 0, _row_stride(q, "q"), block_stride,
                          dim ** -0.5 if scale is None else float(scale), 0.0)
 
 

@@ -283,3 +283,65 @@ def test_captured_graph_follows_the_lengths(sv):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(first["out"], eager["out"]) and torch.equal(first["lse"], eager["lse"])
+
+
+@pytest.mark.parametrize("short", [False, True])
+@pytest.mark.parametrize("dtype,dim", [("bf16", 64), ("bf16", 128), ("f16", 256), ("f32", 64)])
+def test_windows_of_any_width(sv, dtype, dim, short):
+    """The widest windows; short: also rows before position 0 (which see nothing)."""
+    case = C.attend_case([40, 3, 0], [6, 9, 4], 4, 2, dim, 16, dtype, seed=21)
+    if short:
+        case["seq_lens"] = torch.tensor([40, 3, 0], dtype=torch.int32)
+    g = C.on_gpu(case)
+    args = [g[n] for n in ("q", "k_cache", "v_cache", "block_table", "seq_lens", "cu_tokens")]
+    full = sv.kv_paged_attention(*args, lse=True)
+    longest = int(case["seq_lens"].max())
+    for window in (2 ** 31 - 1, 2 ** 31 - 2, 46, 45, 41, 40, 39):
+        r = sv.kv_paged_attention(*args, lse=True, sliding_window=window)
+        torch.cuda.synchronize()
+        same = torch.equal(r["out"], full["out"]) and torch.equal(r["lse"], full["lse"])
+        assert same == (window >= longest), window
+        C.check(C.to64(r["out"]), C.to64(r["lse"]), C.reference(case, window=window), dtype, dim)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_token_ranges_that_overlap_touch_nothing_else(sv, dtype):
+    """Offsets that do not ascend can ask for more tiles than were launched: none
+    is computed then, and the outputs keep their values."""
+    B, n = 12, 160
+    g = C.on_gpu(C.attend_case([500] * B, [n] + [0] * (B - 1), 4, 2, 128, 16, dtype, seed=22))
+    cu = torch.tensor([0, n] * (B // 2) + [0], dtype=torch.int32, device=C.DEV)
+    args = [g[k] for k in ("q", "k_cache", "v_cache", "block_table", "seq_lens")]
+    guard = torch.full((n + 8, 4, 128), 3.0, dtype=g["q"].dtype, device=C.DEV)
+    r = sv.kv_paged_attention(*args, cu, max_new=n,
+                              out=dict(out=guard[4:n + 4], lse=None, workspace=None))
+    torch.cuda.synchronize()
+    assert r["out"].shape[0] == n and (guard == 3.0).all()
+
+
+def test_two_graphs_share_a_workspace(sv):
+    """Two captured calls of different shapes on one workspace, replayed in turn."""
+    names = ("q", "k_cache", "v_cache", "block_table", "seq_lens", "cu_tokens")
+    cases = [C.on_gpu(C.attend_case([6000, 30], [5, 9], 8, 2, 128, 16, "bf16", seed=23)),
+             C.on_gpu(C.attend_case([2500, 900, 7], [1, 1, 1], 4, 4, 64, 8, "f16", seed=24))]
+    alone = [sv.kv_paged_attention(*[c[n] for n in names]) for c in cases]
+    torch.cuda.synchronize()
+    shared = max((r["workspace"] for r in alone), key=lambda w: w.numel())
+    outs = [dict(out=torch.zeros_like(r["out"]), lse=None, workspace=shared) for r in alone]
+    graphs = []
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for c, o in zip(cases, outs):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.stream(s):
+            with torch.cuda.graph(graphs[-1], stream=s):
+                sv.kv_paged_attention(*[c[n] for n in names], out=o)
+    for rep in range(6):
+        for o in outs:
+            o["out"].fill_(2.0)
+        torch.cuda.synchronize()
+        graphs[rep % 2].replay()
+        graphs[1 - rep % 2].replay()
+        torch.cuda.synchronize()
+        for o, r in zip(outs, alone):
+            assert torch.equal(o["out"], r["out"])

@@ -120,7 +120,8 @@ BAD = [(dict(batch=-1), 1), (dict(tokens=-1), 1), (dict(heads=0), 1), (dict(head
        (dict(q_stride=511), 1), (dict(q_stride=516), 3), (dict(block_stride=2047), 1),
        (dict(block_stride=2052), 3), (dict(scale=0.0), 1), (dict(scale=-1.0), 1),
        (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1),
-       (dict(tokens=2 ** 31 - 1), 2)]
+       (dict(scale=3e38), 1), (dict(tokens=2 ** 31 - 1), 2),
+       (dict(tokens=2 ** 27, heads=8, kv_heads=8, dtype=0), 2)]
 
 
 @pytest.mark.parametrize("kw,status", BAD)
@@ -209,3 +210,25 @@ def test_binding_refusals_others(sv):
             sv.kv_cache_append(*args)
     with pytest.raises(TypeError):
         sv.kv_cache_append(k.double(), k.double(), slots, c, c)
+
+
+def test_binding_refuses_overlapping_rows_and_blocks(sv):
+    t = _cpu_tensors()
+    row = torch.zeros((1, 4, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="rows must not overlap"):
+        sv.kv_paged_attention(**{**t, "q": row.expand(3, 4, 64)})
+    wide = torch.zeros((1, 2, 16, 64), dtype=torch.bfloat16).expand(5, 2, 16, 64)
+    with pytest.raises(ValueError, match="blocks of a cache"):
+        sv.kv_paged_attention(**{**t, "k_cache": wide, "v_cache": wide})
+    with pytest.raises(ValueError, match="rows must not overlap"):
+        sv.kv._row_stride(row.expand(3, 4, 64), "k")
+    # one row has no stride to speak of
+    assert sv.kv._row_stride(row, "k") == 0
+    assert sv.kv._caches(wide[:1], wide[:1], torch.bfloat16, wide.device)[4] == 0
+
+
+@pytest.mark.parametrize("name", ["sliding_window", "max_new"])
+@pytest.mark.parametrize("value", [2 ** 31, 2 ** 32 + 4, -2 ** 32 + 1])
+def test_binding_refuses_numbers_beyond_32_bits(sv, name, value):
+    with pytest.raises(ValueError, match="32-bit"):
+        sv.kv_paged_attention(**_cpu_tensors(), **{name: value})
