@@ -93,8 +93,8 @@ struct AttendPlan {
 
 size_t pad256(size_t n) { return (n + 255) / 256 * 256; }
 
-// The kernel for a call: the matrix-core one where types and head size have it,
-// with the smallest tile that takes the rows of one sequence and key head
+// The kernel for a call: the matrix-core one for 16-bit types (at head_dim 40 to
+// 192 it takes an eighth to a thirtieth of the vector units' time), with the smallest tile that takes the rows of one sequence and key head
 // (rows: the caller's max_new, or the batch's mean, times the heads of a group).
 // wgs: items to aim at where keys are split, one for each workgroup the chip
 // holds.  min_units: a split costs a row 8 bytes of partial result per element,
@@ -104,14 +104,14 @@ size_t pad256(size_t n) { return (n + 255) / 256 * 256; }
 sv::AttendShape attend_shape(const spec_kv_attention_desc& d) {
   sv::AttendShape s{};
   const int D = d.head_dim;
-  s.matrix = d.dtype != SV_DTYPE_F32 && (D == 64 || D == 128 || D == 256) && d.num_blocks > 0;
+  s.matrix = d.dtype != SV_DTYPE_F32;
   if (s.matrix) {
     const int64_t mean = d.batch > 0 ? (static_cast<int64_t>(d.tokens) + d.batch - 1) / d.batch : 1;
     const int64_t n = std::min<int64_t>(d.max_new > 0 ? d.max_new : mean, d.tokens);
     const int64_t rows = n * (d.heads / d.kv_heads);
-    s.mt = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 || D == 256 ? 64 : 128;
+    s.mt = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 || D > 128 ? 64 : 128;
     s.kt = s.mt == 128 ? 64 : 32;
-    s.wgs = D == 64 ? (s.mt == 128 ? 768 : 1024) : 512;
+    s.wgs = D <= 64 ? (s.mt == 128 ? 768 : 1024) : 512;
     s.min_units = static_cast<int32_t>(std::max<int64_t>(64, 4 * std::min<int64_t>(rows, s.mt)) /
                                        s.kt);
   } else {
@@ -154,8 +154,10 @@ int32_t make_attend_plan(const spec_kv_attention_desc* d, AttendPlan* p) {
 
   const int64_t group = d->heads / d->kv_heads;
   p->shape = attend_shape(*d);
-  const int64_t cap = std::min<int64_t>(static_cast<int64_t>(d->max_blocks) * d->block_size,
-                                        INT32_MAX);
+  // (without blocks there is no page, and no block 0 for a missing one to read)
+  const int64_t cap = d->num_blocks == 0 ? 0
+                      : std::min<int64_t>(static_cast<int64_t>(d->max_blocks) * d->block_size,
+                                          INT32_MAX);
   p->cap = static_cast<int32_t>(cap);
   // Tiles of all sequences together: sum ceil(n_b * group / mt), sum n_b <= T.
   const int64_t mt = p->shape.mt, kt = p->shape.kt;
@@ -166,7 +168,8 @@ int32_t make_attend_plan(const spec_kv_attention_desc* d, AttendPlan* p) {
   int64_t units = (cap + kt - 1) / kt;
   if (d->sliding_window > 0)
     units = std::min(units, (static_cast<int64_t>(d->sliding_window) + d->tokens) / kt + 2);
-  const int64_t splits = (units + p->shape.min_units - 1) / p->shape.min_units;
+  const int64_t splits =
+      std::max<int64_t>(1, (units + p->shape.min_units - 1) / p->shape.min_units);
   const int64_t slots = splits > 1 ? std::min(2 * want, tiles * splits) : 0;
   const int64_t items = std::min(want + tiles, tiles * splits);
   // 256 threads an item: a launch takes fewer than 2^32
@@ -368,9 +371,9 @@ int32_t kv_paged_attention(const spec_kv_attention_desc* desc, const void* q,
   }
   hipStream_t st = static_cast<hipStream_t>(hip_stream);
   hipError_t err;
-  if (!p.shape.matrix) err = sv::launch_attend_rows(a, d.dtype, st);
-  else if (a.D == 64) err = sv::launch_attend_d64(a, d.dtype, p.shape.mt, st);
-  else if (a.D == 128) err = sv::launch_attend_d128(a, d.dtype, p.shape.mt, st);
+  if (!p.shape.matrix) err = sv::launch_attend_rows(a, st);
+  else if (a.D <= 64) err = sv::launch_attend_d64(a, d.dtype, p.shape.mt, st);
+  else if (a.D <= 128) err = sv::launch_attend_d128(a, d.dtype, p.shape.mt, st);
   else err = sv::launch_attend_d256(a, d.dtype, p.shape.mt, st);
   if (err != hipSuccess) return device_error(err, "paged attention launch");
   if (p.max_slots > 0) {

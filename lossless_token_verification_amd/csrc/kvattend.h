@@ -273,7 +273,7 @@ __device__ __forceinline__ void attend_row(const AttendArgs& a, int token0, int 
   head = h * a.group + (row - j * a.group);
 }
 
-hipError_t launch_attend_rows(const AttendArgs& a, int dtype, hipStream_t st);
+hipError_t launch_attend_rows(const AttendArgs& a, hipStream_t st);
 hipError_t launch_attend_d64(const AttendArgs& a, int dtype, int mt, hipStream_t st);
 hipError_t launch_attend_d128(const AttendArgs& a, int dtype, int mt, hipStream_t st);
 hipError_t launch_attend_d256(const AttendArgs& a, int dtype, int mt, hipStream_t st);

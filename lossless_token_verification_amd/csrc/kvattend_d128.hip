@@ -1,11 +1,10 @@
-// Matrix-core paged attention, head_dim 128.
+// Matrix-core paged attention for head sizes above 64 and up to 128.
 #include "kvattend_mfma.h"
 
 namespace sv {
 
 hipError_t launch_attend_d128(const AttendArgs& a, int dtype, int mt, hipStream_t st) {
-  return dtype == kBF16 ? launch_rows_of<__bf16, 128>(a, mt, st)
-                        : launch_rows_of<_Float16, 128>(a, mt, st);
+  return launch_width<128>(a, dtype, mt, st);
 }
 
 }  // namespace sv

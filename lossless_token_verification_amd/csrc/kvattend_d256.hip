@@ -1,11 +1,10 @@
-// Matrix-core paged attention, head_dim 256.
+// Matrix-core paged attention for head sizes above 128 and up to 256.
 #include "kvattend_mfma.h"
 
 namespace sv {
 
 hipError_t launch_attend_d256(const AttendArgs& a, int dtype, int mt, hipStream_t st) {
-  return dtype == kBF16 ? launch_rows_of<__bf16, 256>(a, mt, st)
-                        : launch_rows_of<_Float16, 256>(a, mt, st);
+  return launch_width<256>(a, dtype, mt, st);
 }
 
 }  // namespace sv

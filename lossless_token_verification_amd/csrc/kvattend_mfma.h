@@ -1,5 +1,5 @@
-// Paged attention on the matrix cores (bf16 / f16 caches, head_dim 64, 128 or
-// 256).
+// Paged attention on the matrix cores (bf16 / f16 caches; head_dim 64, 128 and
+// 256, and every other one in the next of these, the rest of a row zero in LDS).
 //
 // One workgroup takes up to MT query rows of a sequence and key head (the
 // heads of a group and the new tokens side by side, so a key is read once for
@@ -24,6 +24,17 @@
 // by 16-byte vectors (swz_k, swz_v) so that the operand reads of either product
 // spread over all banks.  A row's page comes from the block table NB units
 // before its loads, so that no wait for a table entry drains the ring.
+//
+// What bounds it and what it measured (bf16, 32 query and 8 key heads of 128):
+// up to 64 rows the pages' bandwidth (B = 256 verifications of 9 tokens over 512
+// to 4096 positions: 2.60 GB in 437 us, 5.95 TB/s; B = 4 single tokens over 90000
+// to 131071: 2.08 GB in 322 us, 6.5 TB/s; a plain read of such an amount runs at
+// 6.9).  With 128 rows the matrix cores and the exponentials in turn, at the
+// clock that the power limit leaves (1.96 GHz): 4 prompts of 2048 to 4096 tokens
+// 332 GF in 385 to 402 us, 830 to 860 TF; 16384 tokens 1000 TF (head_dim 64: 870).
+// Other head sizes cost what the next of the three costs (B = 64, 9 tokens over
+// 2300 positions: 109 us at 80 and 96, 175 us at 192, against 1.09, 1.08 and 2.02
+// ms on the vector units).
 #pragma once
 
 #include <type_traits>
@@ -117,9 +128,11 @@ __device__ __forceinline__ int fresh(int x) {
 
 // RW: query rows per wavefront (16 or 32, the matrix instruction's width), W
 // wavefronts with different rows; units of KT positions in a ring of NB buffers.
-template <typename T_, int D_, int RW_, int W_, int KT_, int NB_>
+// kPad: head_dim is less than D.
+template <typename T_, int D_, bool kPad_, int RW_, int W_, int KT_, int NB_>
 struct AttendCfg {
   using T = T_;
+  static constexpr bool kPad = kPad_;
   static constexpr int D = D_, RW = RW_, W = W_, KT = KT_, NB = NB_;
   static constexpr int MT = RW * W;
   static constexpr int NV = D / 8;                 // vectors of a row
@@ -185,6 +198,7 @@ attend_mfma_kernel(AttendArgs a) {
   __shared__ AttendPlanShared<C::W> plan;
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int dim = C::kPad ? a.D : D, nv = dim / 8;   // elements and vectors of a row
   const int x = blockIdx.x / a.kv_heads, h = blockIdx.x - x * a.kv_heads;
   AttendItem it;
   if (!attend_find<C::MT, KT, C::W>(a, x, a.max_slots > 0 && blockIdx.x == 0, plan, it)) return;
@@ -205,10 +219,13 @@ attend_mfma_kernel(AttendArgs a) {
     const int key_first = a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
     see_lo = key_last >= key_first ? key_first : INT32_MAX;
     see_span = key_last >= key_first ? key_last - key_first : 0;
-    const T* qr = static_cast<const T*>(a.q) + token * a.q_stride + static_cast<int64_t>(head) * D;
+    const T* qr = static_cast<const T*>(a.q) + token * a.q_stride + static_cast<int64_t>(head) * dim;
 #pragma unroll
-    for (int s = 0; s < QS; ++s)
-      qf[s] = reinterpret_cast<const u32x4*>(qr)[s * (RW == 32 ? 2 : 4) + hi_lane];
+    for (int s = 0; s < QS; ++s) {
+      const int v = s * (RW == 32 ? 2 : 4) + hi_lane;
+      qf[s] = u32x4{0, 0, 0, 0};
+      if (!C::kPad || v < nv) qf[s] = reinterpret_cast<const u32x4*>(qr)[v];
+    }
   }
   // positions every row of the tile may see: units inside need no mask
   const int all_hi = min(it.pos0 + fast_div(it.row0, a.grp), it.key_hi - 1);
@@ -226,7 +243,7 @@ attend_mfma_kernel(AttendArgs a) {
     const int key = nearest(base);
     const int r = key - fast_div(key, a.bs) * a.block_size;
     const int safe = id >= 0 && id < a.num_blocks ? id : 0;
-    return safe * a.block_stride + (head_off + r) * D;
+    return safe * a.block_stride + (head_off + r) * dim;
   };
   auto paged = [&](int id) -> uint64_t { return __ballot(id >= 0 && id < a.num_blocks); };
 
@@ -238,9 +255,11 @@ attend_mfma_kernel(AttendArgs a) {
   // Loads the unit at position `base`; off: offsets of 64 positions, the unit's
   // from lane `from` on.  Inside the item's range, with whole pages of rows, a
   // load's address is one lane's offset plus a lane constant, so the offset
-  // moves through scalar registers; otherwise every lane fetches its row's.
+  // moves through scalar registers; otherwise every lane fetches its row's.  Lanes
+  // of vectors that a row does not have (kPad) load nothing: those places of a
+  // buffer are the same in every unit and hold the zeros they started with.
   auto load_unit = [&](int base, int64_t off, int from, uint16_t* sb) {
-    constexpr int kUnroll = C::LOADS > 8 ? 4 : C::LOADS;
+    constexpr int kUnroll = C::LOADS > (C::kPad ? 4 : 8) ? 4 : C::LOADS;
     int lk = lslot ^ swz_k<D>(lq), lv = lslot ^ swz_v<D>(lq);
     if (D != 128 || C::LOADS > 4) {   // registers are short: formed at each load
       lk = fresh(lk);
@@ -248,7 +267,7 @@ attend_mfma_kernel(AttendArgs a) {
     }
     if (whole_rows && base >= it.key_lo && base + KT <= it.key_hi) {
       const int lo = static_cast<int>(off), hi = static_cast<int>(off >> 32);
-      const uint32_t lane_row = lq * D * 2;
+      const uint32_t lane_row = lq * dim * 2;
 #pragma unroll kUnroll
       for (int i = 0; i < C::LOADS; ++i) {
         const int j = wave + i * C::W;               // which RPL rows
@@ -257,8 +276,10 @@ attend_mfma_kernel(AttendArgs a) {
         const int64_t ro = static_cast<int64_t>((static_cast<uint64_t>(r1) << 32) | r0);
         const uint32_t ko = lane_row + (lk ^ swz_k<D>(j * RPL)) * 16;
         const uint32_t vo = lane_row + (lv ^ swz_v<D>(j * RPL)) * 16;
-        load_lds<C::kOnce>(reinterpret_cast<const char*>(kb + ro) + ko, sb + j * 512);
-        load_lds<C::kOnce>(reinterpret_cast<const char*>(vb + ro) + vo, sb + kV + j * 512);
+        if (!C::kPad || (lk ^ swz_k<D>(j * RPL)) < nv)
+          load_lds<C::kOnce>(reinterpret_cast<const char*>(kb + ro) + ko, sb + j * 512);
+        if (!C::kPad || (lv ^ swz_v<D>(j * RPL)) < nv)
+          load_lds<C::kOnce>(reinterpret_cast<const char*>(vb + ro) + vo, sb + kV + j * 512);
       }
       asm volatile("; scalar addresses");   // keeps the two forms from being merged
       return;
@@ -267,8 +288,9 @@ attend_mfma_kernel(AttendArgs a) {
     for (int i = 0; i < C::LOADS; ++i) {
       const int j = wave + i * C::W;
       const int64_t ro = __shfl(static_cast<long long>(off), from + j * RPL + lq, kWave);
-      load_lds<C::kOnce>(kb + ro + (lk ^ swz_k<D>(j * RPL)) * 8, sb + j * 512);
-      load_lds<C::kOnce>(vb + ro + (lv ^ swz_v<D>(j * RPL)) * 8, sb + kV + j * 512);
+      const int vk = lk ^ swz_k<D>(j * RPL), vv = lv ^ swz_v<D>(j * RPL);
+      if (!C::kPad || vk < nv) load_lds<C::kOnce>(kb + ro + vk * 8, sb + j * 512);
+      if (!C::kPad || vv < nv) load_lds<C::kOnce>(vb + ro + vv * 8, sb + kV + j * 512);
     }
   };
 
@@ -440,19 +462,22 @@ attend_mfma_kernel(AttendArgs a) {
     if (row >= it.rows) return;
     if (it.splits > 1) {
       const int64_t p = (static_cast<int64_t>(it.slot) * a.kv_heads + h) * C::MT + row;
-      float* po = a.part_o + p * D + t * RW + 4 * hi_lane;
+      const int e = t * RW + 4 * hi_lane;       // first element
+      float* po = a.part_o + p * dim + e;
 #pragma unroll
       for (int r = 0; r < SR; r += 4)
-        *reinterpret_cast<f32x4*>(po + r * 2) = f32x4{x[r], x[r + 1], x[r + 2], x[r + 3]};
+        if (!C::kPad || e + r * 2 < dim)
+          *reinterpret_cast<f32x4*>(po + r * 2) = f32x4{x[r], x[r + 1], x[r + 2], x[r + 3]};
       return;
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     int token, head;
     attend_row(a, it.token0, it.row0 + fresh(row), h, token, head);
-    T* po = static_cast<T*>(a.out) + (static_cast<int64_t>(token) * a.heads + head) * D + t * RW +
-            4 * hi_lane;
+    const int e = t * RW + 4 * hi_lane;
+    T* po = static_cast<T*>(a.out) + (static_cast<int64_t>(token) * a.heads + head) * dim + e;
 #pragma unroll
     for (int r = 0; r < SR; r += 4) {
+      if (C::kPad && e + r * 2 >= dim) continue;
       typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
       *reinterpret_cast<u32x2*>(po + r * 2) =
           u32x2{pack2<T>(x[r] * inv, x[r + 1] * inv), pack2<T>(x[r + 2] * inv, x[r + 3] * inv)};
@@ -487,6 +512,17 @@ attend_mfma_kernel(AttendArgs a) {
     // (one row), which keeps the number of loads under way a constant.  The table
     // entries of turn q of the ring (units q NB ..) are loaded into LDS as well,
     // one turn before their use, so that nothing but the counted waits waits.
+    if (C::kPad) {
+      auto clear = [&](uint16_t* sb) {
+        for (int i = tid; i < 2 * kV / 8; i += C::W * kWave)
+          reinterpret_cast<u32x4*>(sb)[i] = u32x4{0, 0, 0, 0};
+      };
+      clear(sb0);
+      clear(sb1);
+      if (NB > 2) clear(sb2);
+      if (NB > 3) clear(sb3);
+      __syncthreads();
+    }
     uint16_t* const ring[4] = {sb0, sb1, sb2, sb3};
     const int first = it.u0 * KT;
     int32_t* const ids = sid + wave * C::SUPER;
@@ -589,10 +625,10 @@ attend_mfma_kernel(AttendArgs a) {
     const int r = i * RPL + lq;
     const u32x4 w = *reinterpret_cast<const u32x4*>(turned + r * (D * 2) +
                                                     ((lslot ^ swz_k<D>(r)) << 4));
-    if (wave * RW + r < it.rows) {
+    if (wave * RW + r < it.rows && (!C::kPad || lslot < nv)) {
       int token, head;
       attend_row(a, it.token0, it.row0 + wave * RW + r, h, token, head);
-      T* po = static_cast<T*>(a.out) + (static_cast<int64_t>(token) * a.heads + head) * D;
+      T* po = static_cast<T*>(a.out) + (static_cast<int64_t>(token) * a.heads + head) * dim;
       reinterpret_cast<u32x4*>(po)[lslot] = w;
     }
   }
@@ -609,19 +645,28 @@ void launch_cfg(const AttendArgs& a, hipStream_t st) {
 // matrix and vector units: units of 64 positions, half the barriers.  Rows of
 // head_dim 256 leave LDS for two buffers and registers for 16 query rows a
 // wavefront, 64 a tile.
-template <typename T, int D>
+template <typename T, int D, bool kPad>
 hipError_t launch_rows_of(const AttendArgs& a, int mt, hipStream_t st) {
   constexpr bool kBig = D == 256;
   constexpr int NB = kBig ? 2 : 4, RW = kBig ? 16 : 32;
   switch (mt) {
-    case 16: launch_cfg<AttendCfg<T, D, 16, 1, 32, NB>>(a, st); break;
-    case 32: launch_cfg<AttendCfg<T, D, RW, 32 / RW, 32, NB>>(a, st); break;
-    case 64: launch_cfg<AttendCfg<T, D, RW, 64 / RW, 32, NB>>(a, st); break;
+    case 16: launch_cfg<AttendCfg<T, D, kPad, 16, 1, 32, NB>>(a, st); break;
+    case 32: launch_cfg<AttendCfg<T, D, kPad, RW, 32 / RW, 32, NB>>(a, st); break;
+    case 64: launch_cfg<AttendCfg<T, D, kPad, RW, 64 / RW, 32, NB>>(a, st); break;
     default:
-      if constexpr (!kBig) launch_cfg<AttendCfg<T, D, 32, 4, 64, 2>>(a, st);
+      if constexpr (!kBig) launch_cfg<AttendCfg<T, D, kPad, 32, 4, 64, 2>>(a, st);
       else return hipErrorInvalidValue;
   }
   return hipGetLastError();
+}
+
+template <int D>
+hipError_t launch_width(const AttendArgs& a, int dtype, int mt, hipStream_t st) {
+  if (dtype == kBF16)
+    return a.D == D ? launch_rows_of<__bf16, D, false>(a, mt, st)
+                    : launch_rows_of<__bf16, D, true>(a, mt, st);
+  return a.D == D ? launch_rows_of<_Float16, D, false>(a, mt, st)
+                  : launch_rows_of<_Float16, D, true>(a, mt, st);
 }
 
 }  // namespace sv

@@ -254,6 +254,12 @@ def test_empty_calls(sv):
                               case["block_table"], case["seq_lens"], case["cu_tokens"], lse=True)
     torch.cuda.synchronize()
     assert (r["out"] == 0).all() and torch.isneginf(r["lse"]).all()
+    # tables without columns
+    r = sv.kv_paged_attention(case["q"], case["k_cache"], case["v_cache"],
+                              case["block_table"][:, :0].contiguous(), case["seq_lens"],
+                              case["cu_tokens"], lse=True)
+    torch.cuda.synchronize()
+    assert (r["out"] == 0).all() and torch.isneginf(r["lse"]).all()
 
 
 def test_captured_graph_follows_the_lengths(sv):
@@ -345,3 +351,28 @@ def test_two_graphs_share_a_workspace(sv):
         torch.cuda.synchronize()
         for o, r in zip(outs, alone):
             assert torch.equal(o["out"], r["out"])
+
+
+@pytest.mark.parametrize("dim", [8, 24, 40, 56, 72, 80, 96, 120, 136, 160, 192, 248])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_head_sizes_between(sv, dtype, dim):
+    """Head sizes that fill a part of the matrix kernel's rows: every tile height,
+    with split keys and without, windows, neighbouring memory of NaN."""
+    for i, (ctx, new, heads, kv, bs, window) in enumerate([
+            ([3000, 5], [1, 1], 4, 2, 16, 0), ([70, 400], [9, 20], 2, 2, 24, 0),
+            ([33, 0, 600], [40, 7, 50], 3, 3, 5, 100), ([10, 700], [150, 60], 4, 2, 32, 0),
+            ([2500], [130], 2, 1, 16, 0)]):
+        case = C.attend_case(ctx, new, heads, kv, dim, bs, dtype, seed=40 + i, lead=2, tail=3,
+                             fused=i % 2 == 1)
+        g = C.on_gpu(case)
+        T = case["q"].shape[0]
+        guard = torch.full((T + 2, heads, dim), 7.0, dtype=C.DT[dtype], device=C.DEV)
+        lse = torch.full((T, heads), 7.0, device=C.DEV)
+        sv.kv_paged_attention(*[g[n] for n in ("q", "k_cache", "v_cache", "block_table",
+                                               "seq_lens", "cu_tokens")], sliding_window=window,
+                              max_new=max(new),
+                              out=dict(out=guard[1:T + 1], lse=lse, workspace=None))
+        torch.cuda.synchronize()
+        C.check(C.to64(guard[1:T + 1]), C.to64(lse), C.reference(case, window=window), dtype, dim,
+                (i, dim))
+        assert (guard[:3] == 7.0).all() and (guard[-4:] == 7.0).all() and (lse[-3:] == 7.0).all()
