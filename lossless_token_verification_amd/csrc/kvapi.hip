@@ -93,14 +93,18 @@ struct AttendPlan {
 
 size_t pad256(size_t n) { return (n + 255) / 256 * 256; }
 
-// The kernel for a call: the matrix-core one for 16-bit types (at head_dim 40 to
-// 192 it takes an eighth to a thirtieth of the vector units' time), with the smallest tile that takes the rows of one sequence and key head
-// (rows: the caller's max_new, or the batch's mean, times the heads of a group).
-// wgs: items to aim at where keys are split, one for each workgroup the chip
-// holds.  min_units: a split costs a row 8 bytes of partial result per element,
-// written and read, a position 4 of cache; 4 positions per row and 64 at least
-// measured best where splits are that short, on a chip that is not full (9 rows
-// x 4 heads over 4000 positions: 26 us with 16 positions per row, 17 with 4).
+// The kernel for a call: the matrix-core one for 16-bit types (an eighth to a
+// thirtieth of the vector units' time at head_dim 40 to 192), with the smallest
+// tile that takes the rows of one sequence and key head (rows: the caller's
+// max_new, or the batch's mean, times the heads of a group).  Smaller tiles read
+// the keys again, larger ones compute rows that are not there (head_dim 128, B =
+// 128 over 2300 positions: 36 rows 387 us in tiles of 32, 214 of 64, 237 of 128; 4
+// rows 195, 198, 225).  wgs: items to aim at where keys are split, one for each
+// workgroup the chip holds.  min_units: a split costs a row 8 bytes of partial
+// result per element, written and read, a position 4 of cache; 4 positions per
+// row and 64 at least measured best where splits are that short, on a chip that is
+// not full (9 rows x 4 heads over 4000 positions: 26 us with 16 positions per row,
+// 17 with 4).
 sv::AttendShape attend_shape(const spec_kv_attention_desc& d) {
   sv::AttendShape s{};
   const int D = d.head_dim;
@@ -109,7 +113,7 @@ sv::AttendShape attend_shape(const spec_kv_attention_desc& d) {
     const int64_t mean = d.batch > 0 ? (static_cast<int64_t>(d.tokens) + d.batch - 1) / d.batch : 1;
     const int64_t n = std::min<int64_t>(d.max_new > 0 ? d.max_new : mean, d.tokens);
     const int64_t rows = n * (d.heads / d.kv_heads);
-    s.mt = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 || D > 128 ? 64 : 128;
+    s.mt = rows <= 32 ? 32 : rows <= 64 || D > 128 ? 64 : 128;
     s.kt = s.mt == 128 ? 64 : 32;
     s.wgs = D <= 64 ? (s.mt == 128 ? 768 : 1024) : 512;
     s.min_units = static_cast<int32_t>(std::max<int64_t>(64, 4 * std::min<int64_t>(rows, s.mt)) /

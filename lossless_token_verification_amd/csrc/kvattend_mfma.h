@@ -27,11 +27,11 @@
 //
 // What bounds it and what it measured (bf16, 32 query and 8 key heads of 128):
 // up to 64 rows the pages' bandwidth (B = 256 verifications of 9 tokens over 512
-// to 4096 positions: 2.60 GB in 437 us, 5.95 TB/s; B = 4 single tokens over 90000
-// to 131071: 2.08 GB in 322 us, 6.5 TB/s; a plain read of such an amount runs at
+// to 4096 positions: 2.60 GB in 432 us, 6.0 TB/s; B = 4 single tokens over 90000
+// to 131071: 2.08 GB in 327 us, 6.4 TB/s; a plain read of such an amount runs at
 // 6.9).  With 128 rows the matrix cores and the exponentials in turn, at the
 // clock that the power limit leaves (1.96 GHz): 4 prompts of 2048 to 4096 tokens
-// 332 GF in 385 to 402 us, 830 to 860 TF; 16384 tokens 1000 TF (head_dim 64: 870).
+// 332 GF in 385 to 407 us, 815 to 860 TF; 16384 tokens 1000 TF (head_dim 64: 870).
 // Other head sizes cost what the next of the three costs (B = 64, 9 tokens over
 // 2300 positions: 109 us at 80 and 96, 175 us at 192, against 1.09, 1.08 and 2.02
 // ms on the vector units).
@@ -640,19 +640,22 @@ void launch_cfg(const AttendArgs& a, hipStream_t st) {
                      dim3(C::W * kWave), 0, st, a);
 }
 
-// Tiles of 16, 32, 64 and 128 rows.  Up to 64 rows the cache's bandwidth bounds
-// the kernel: short units, most of them under way.  128 rows are bound by the
-// matrix and vector units: units of 64 positions, half the barriers.  Rows of
-// head_dim 256 leave LDS for two buffers and registers for 16 query rows a
-// wavefront, 64 a tile.
+// Tiles of 32, 64 and 128 rows.  Up to 64 rows the cache's bandwidth bounds the
+// kernel: short units, most of them under way, and 16 rows a wavefront, since
+// more wavefronts start and load a unit faster (32 rows: 36 rows over 500
+// positions at B = 256 130 us against 122; a 16-row tile of one wavefront: single
+// tokens there 126 us against 107, over 1000 positions at B = 1 14.5 against 12.4,
+// over 110000 at B = 4 274 against 282).  128 rows are bound by the matrix and
+// vector units: 32 rows a wavefront and units of 64 positions, half the operand
+// reads and barriers.  Rows of head_dim 256 leave LDS for two buffers and
+// registers for 16 query rows a wavefront, 64 a tile.
 template <typename T, int D, bool kPad>
 hipError_t launch_rows_of(const AttendArgs& a, int mt, hipStream_t st) {
   constexpr bool kBig = D == 256;
-  constexpr int NB = kBig ? 2 : 4, RW = kBig ? 16 : 32;
+  constexpr int NB = kBig ? 2 : 4;
   switch (mt) {
-    case 16: launch_cfg<AttendCfg<T, D, kPad, 16, 1, 32, NB>>(a, st); break;
-    case 32: launch_cfg<AttendCfg<T, D, kPad, RW, 32 / RW, 32, NB>>(a, st); break;
-    case 64: launch_cfg<AttendCfg<T, D, kPad, RW, 64 / RW, 32, NB>>(a, st); break;
+    case 32: launch_cfg<AttendCfg<T, D, kPad, 16, 2, 32, NB>>(a, st); break;
+    case 64: launch_cfg<AttendCfg<T, D, kPad, 16, 4, 32, NB>>(a, st); break;
     default:
       if constexpr (!kBig) launch_cfg<AttendCfg<T, D, kPad, 32, 4, 64, 2>>(a, st);
       else return hipErrorInvalidValue;

@@ -19,7 +19,7 @@ HIPCC = "/opt/rocm/bin/hipcc"
                     reason="hipcc is not installed")
 @pytest.mark.parametrize("src,kernels", [
     ("kvblocks.hip", 3), ("kvappend.hip", 3), ("kvattend_rows.hip", 6),
-    ("kvattend_d64.hip", 16), ("kvattend_d128.hip", 16), ("kvattend_d256.hip", 12)])
+    ("kvattend_d64.hip", 12), ("kvattend_d128.hip", 12), ("kvattend_d256.hip", 8)])
 def test_no_kernel_uses_scratch(src, kernels):
     cmd = [HIPCC, "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Xclang",
            "-target-feature", "-Xclang", "-packed-fp32-ops", "--cuda-device-only", "-c",
