@@ -50,8 +50,8 @@ extern "C" {
 int32_t spec_kv_abi_version(void);
 
 /* Grows block tables by num_new tokens per sequence and maps the tokens to
- * slots.  Sequence b holds L = seq_lens[b] tokens and gets n = num_new[b] more,
- * for which it needs ceil((L + n) / bs) - ceil(L / bs) blocks.
+ * slots (batch at most 2^24).  Sequence b holds L = seq_lens[b] tokens and gets
+ * n = num_new[b] more, for which it needs ceil((L + n) / bs) - ceil(L / bs) blocks.
  *
  * The pool is a stack: free_blocks[0 .. *free_count), popped from its end.
  * First the blocks freed[b, 0 .. num_freed[b]) of every sequence in order
@@ -69,8 +69,8 @@ int32_t spec_kv_abi_version(void);
  *   freed_blocks [B, max_freed] device int32 or NULL: ids to push
  *   num_freed    [B]  device int32 (required with freed_blocks)
  *   max_tokens   rows of the packed token arrays (the largest sum of num_new
- *                this call takes; a batch padded for a captured graph has more
- *                rows than tokens)
+ *                this call takes, 2^30 at most; a batch padded for a captured
+ *                graph has more rows than tokens)
  *   new_lens     [B]  out: L + n, or L where the sequence was not served
  *   num_taken    [B]  out: blocks taken; -1: n < 0, L < 0, L + n beyond the
  *                table or beyond INT32_MAX, or tokens beyond max_tokens; -2:
@@ -123,7 +123,7 @@ int32_t kv_cache_append(const spec_kv_append_desc* desc, const void* k, const vo
                         void* hip_stream);
 
 typedef struct {
-  int32_t batch;          /* B >= 0                                              */
+  int32_t batch;          /* B in [0, 2^24]                                      */
   int32_t tokens;         /* T >= 0 query rows; T * heads < 2^31                 */
   int32_t heads;          /* query heads, a multiple of kv_heads                 */
   int32_t kv_heads;       /* >= 1; head h reads key head h / (heads / kv_heads)   */

@@ -46,6 +46,8 @@ int32_t check_ptr(const void* p, bool required, uintptr_t align, const char* nam
 constexpr int32_t kMaxHeads = 1 << 16;
 constexpr int32_t kMaxRowDim = 1 << 12;   // head_dim of a cache append
 constexpr int64_t kMaxStride = int64_t{1} << 40;
+constexpr int32_t kMaxBatch = 1 << 24;
+constexpr int32_t kMaxRows = 1 << 30;     // rows of an extension's token arrays
 constexpr int64_t kMaxWorkgroups = int64_t{1} << 24;
 
 int dtype_bytes(int dtype) { return dtype == SV_DTYPE_F32 ? 4 : 2; }
@@ -132,6 +134,7 @@ int32_t make_attend_plan(const spec_kv_attention_desc* d, AttendPlan* p) {
   if (d->reserved != 0 || d->reserved_f != 0.0f)
     return fail(SV_ERR_INVALID_ARG, "reserved fields must be 0");
   if (d->batch < 0) return fail(SV_ERR_INVALID_ARG, "batch < 0");
+  if (d->batch > kMaxBatch) return fail(SV_ERR_UNSUPPORTED, "batch > %d", kMaxBatch);
   if (d->tokens < 0) return fail(SV_ERR_INVALID_ARG, "tokens < 0");
   if (d->max_blocks < 0) return fail(SV_ERR_INVALID_ARG, "max_blocks < 0");
   if (d->sliding_window < 0) return fail(SV_ERR_INVALID_ARG, "sliding_window < 0");
@@ -208,11 +211,13 @@ int32_t kv_blocktable_extend(int32_t batch, int32_t max_blocks, int32_t block_si
                              int32_t* num_taken, int32_t* free_left, int32_t* cu_tokens,
                              int64_t* slot_map, int32_t* positions, void* hip_stream) {
   if (batch < 0) return fail(SV_ERR_INVALID_ARG, "batch < 0");
+  if (batch > kMaxBatch) return fail(SV_ERR_UNSUPPORTED, "batch > %d", kMaxBatch);
   if (max_blocks < 0) return fail(SV_ERR_INVALID_ARG, "max_blocks < 0");
   if (block_size < 1) return fail(SV_ERR_INVALID_ARG, "block_size < 1");
   if (free_capacity < 0) return fail(SV_ERR_INVALID_ARG, "free_capacity < 0");
   if (max_freed < 0) return fail(SV_ERR_INVALID_ARG, "max_freed < 0");
   if (max_tokens < 0) return fail(SV_ERR_INVALID_ARG, "max_tokens < 0");
+  if (max_tokens > kMaxRows) return fail(SV_ERR_UNSUPPORTED, "max_tokens > %d", kMaxRows);
   const bool any = batch > 0;
   SV_TRY(check_ptr(block_table, any && max_blocks > 0, 4, "block_table"));
   SV_TRY(check_ptr(seq_lens, any, 4, "seq_lens"));

@@ -58,31 +58,32 @@ def set_signatures(lib):
                                        ctypes.c_size_t, P]
 
 
-def _call(fn, device, *args):
-    """Calls an entry point on torch's current stream of ``device``, with that
+def _call(fn, index, *args):
+    """Calls an entry point on torch's current stream of GPU ``index``, with that
     device current (the null stream belongs to the current device)."""
-    index = device.index
     if torch._C._cuda_getDevice() == index:
         status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if status:
         _pkg._check(status)
 
 
 def _gpu(t):
-    """The device of a GPU tensor."""
+    """The device index of a GPU tensor."""
     if not t.is_cuda:
         raise ValueError("tensors must be on a GPU")
-    return t.device
+    return t.get_device()
 
 
-def _tensor(t, name, dtype, shape, device):
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
+def _tensor(t, name, dtype, shape, index):
+    """The pointer of a contiguous tensor of this dtype and shape on GPU ``index``."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or \
+            t.get_device() != index:
         raise ValueError(f"{name} must be a contiguous {str(dtype)[6:]} tensor of shape "
-                         f"{list(shape)} on {device}, got {str(t.dtype)[6:]} {list(t.shape)} on "
-                         f"{t.device}")
+                         f"{list(shape)} on cuda:{index}, got {str(t.dtype)[6:]} "
+                         f"{list(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
@@ -146,7 +147,7 @@ def kv_blocktable_extend(block_table, seq_lens, num_new, free_blocks, free_count
     dict of an earlier call of the same shape, whose tensors are reused; its
     new_lens may be ``seq_lens`` and its free_left ``free_count``."""
     lib = _pkg.library()
-    dev, i32 = _gpu(block_table), torch.int32
+    dev, i32 = _gpu(block_table), torch.int32      # dev: its index
     B, width = block_table.shape
     T = _i32(max_tokens, "max_tokens")
     if T < 0:
@@ -161,16 +162,17 @@ def kv_blocktable_extend(block_table, seq_lens, num_new, free_blocks, free_count
     if freed_blocks is not None:
         if num_freed is None:
             raise ValueError("freed_blocks needs num_freed")
+        if freed_blocks.dim() != 2:
+            raise ValueError("freed_blocks must be [B, max_freed]")
         max_freed = freed_blocks.shape[1]
         pf = _tensor(freed_blocks, "freed_blocks", i32, (B, max_freed), dev) if max_freed else None
         pn = _tensor(num_freed, "num_freed", i32, (B,), dev)
     if out is None:
-        out = dict(new_lens=torch.empty(B, dtype=i32, device=dev),
-                   num_taken=torch.empty(B, dtype=i32, device=dev),
-                   free_left=torch.empty(1, dtype=i32, device=dev),
-                   cu_tokens=torch.empty(B + 1, dtype=i32, device=dev),
-                   slot_map=torch.empty(T, dtype=torch.int64, device=dev),
-                   positions=torch.empty(T, dtype=i32, device=dev))
+        on = dict(dtype=i32, device=block_table.device)
+        out = dict(new_lens=torch.empty(B, **on), num_taken=torch.empty(B, **on),
+                   free_left=torch.empty(1, **on), cu_tokens=torch.empty(B + 1, **on),
+                   slot_map=torch.empty(T, dtype=torch.int64, device=block_table.device),
+                   positions=torch.empty(T, **on))
     _call(lib.kv_blocktable_extend, dev, B, width, _i32(block_size, "block_size"), p[0], p[1], p[2], p[3],
           free_blocks.numel(), pc, pf, max_freed, pn, T,
           _tensor(out["new_lens"], "out new_lens", i32, (B,), dev),
@@ -191,9 +193,9 @@ def kv_cache_append(k, v, slot_map, k_cache, v_cache):
     if k.dtype not in _CODES:
         raise TypeError(f"k must be float32, bfloat16 or float16, got {k.dtype}")
     dev = _gpu(k)
-    nb, kv, bs, dim, block_stride = _caches(k_cache, v_cache, k.dtype, dev)
+    nb, kv, bs, dim, block_stride = _caches(k_cache, v_cache, k.dtype, k.device)
     if k.dim() != 3 or k.shape[1:] != (kv, dim) or v.shape != k.shape or v.dtype != k.dtype or \
-            v.device != dev:
+            v.get_device() != dev:
         raise ValueError(f"k and v must be [T, {kv}, {dim}] of one dtype on one device")
     T = _i32(k.shape[0], "T")
     desc = AppendDesc(T, kv, dim, bs, nb, _CODES[k.dtype], _row_stride(k, "k"),
@@ -246,9 +248,9 @@ def kv_paged_attention(q, k_cache, v_cache, block_table, seq_lens, cu_tokens, *,
     pl = _tensor(seq_lens, "seq_lens", torch.int32, (B,), dev)
     pc = _tensor(cu_tokens, "cu_tokens", torch.int32, (B + 1,), dev)
     if out is None:
-        out = dict(out=torch.empty((T, heads, dim), dtype=q.dtype, device=dev),
-                   lse=torch.empty((T, heads), dtype=torch.float32, device=dev) if lse else None,
-                   workspace=None)
+        out = dict(out=torch.empty((T, heads, dim), dtype=q.dtype, device=q.device),
+                   lse=torch.empty((T, heads), dtype=torch.float32, device=q.device)
+                   if lse else None, workspace=None)
     elif lse and out["lse"] is None:
         raise ValueError("out holds no lse tensor")
     if workspace is None:
@@ -256,8 +258,8 @@ def kv_paged_attention(q, k_cache, v_cache, block_table, seq_lens, cu_tokens, *,
     if workspace is None:
         need = lib.kv_paged_attention_workspace_bytes(ctypes.byref(desc))
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif workspace.device != dev or not workspace.is_contiguous():
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on q's device")
     out["workspace"] = workspace
     _call(lib.kv_paged_attention, dev, ctypes.byref(desc), q.data_ptr(), k_cache.data_ptr(),

@@ -56,6 +56,7 @@ def _extend(sv, **kw):
     (dict(table=None), 1), (dict(lens=None), 1), (dict(new=None), 1), (dict(free=None), 1),
     (dict(count=None), 1), (dict(freed=P, max_freed=1), 1), (dict(new_lens=None), 1),
     (dict(taken=None), 1), (dict(left=None), 1), (dict(cu=None), 1), (dict(slots=None), 1),
+    (dict(batch=(1 << 24) + 1), 2), (dict(max_tokens=(1 << 30) + 1), 2),
     (dict(table=ctypes.c_void_p(0x1002)), 3), (dict(slots=ctypes.c_void_p(0x1004)), 3),
     (dict(positions=ctypes.c_void_p(0x1001)), 3)])
 def test_extend_refusals(sv, kw, status):
@@ -111,7 +112,7 @@ def _ws(sv, kv, **kw):
         ctypes.byref(kv.AttentionDesc(*d.values())))
 
 
-BAD = [(dict(batch=-1), 1), (dict(tokens=-1), 1), (dict(heads=0), 1), (dict(heads=7), 1),
+BAD = [(dict(batch=-1), 1), (dict(batch=(1 << 24) + 1), 2), (dict(tokens=-1), 1), (dict(heads=0), 1), (dict(heads=7), 1),
        (dict(heads=1 << 17, kv_heads=1), 2), (dict(kv_heads=0), 1), (dict(head_dim=60), 2),
        (dict(head_dim=264), 2), (dict(head_dim=0), 1), (dict(block_size=0), 1),
        (dict(num_blocks=-1), 1), (dict(num_blocks=1 << 30), 2), (dict(max_blocks=-1), 1),
@@ -200,6 +201,10 @@ def test_binding_refusals_others(sv):
         sv.kv_blocktable_extend(table, i, i, free, one, 16, -1)
     with pytest.raises(ValueError):
         sv.kv_blocktable_extend(table, i, i, free, one, 16, 4, freed_blocks=table)
+    with pytest.raises(ValueError):
+        sv.kv_blocktable_extend(table, i, i, free, one, 16, 2 ** 32 + 4)
+    with pytest.raises(ValueError):
+        sv.kv_blocktable_extend(table, i, i, free, one, 2 ** 32 + 16, 4)
     c = torch.zeros((5, 2, 16, 64), dtype=torch.bfloat16)
     k = torch.zeros((3, 2, 64), dtype=torch.bfloat16)
     slots = torch.zeros(3, dtype=torch.int64)
