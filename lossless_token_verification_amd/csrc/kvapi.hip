@@ -117,7 +117,7 @@ sv::AttendShape attend_shape(const spec_kv_attention_desc& d) {
     const int64_t rows = n * (d.heads / d.kv_heads);
     s.mt = rows <= 32 ? 32 : rows <= 64 || D > 128 ? 64 : 128;
     s.kt = s.mt == 128 ? 64 : 32;
-    s.wgs = D <= 64 ? (s.mt == 128 ? 768 : 1024) : 512;
+    s.wgs = D > 128 || (D > 64 && s.mt == 128) ? 512 : D > 64 || s.mt == 128 ? 768 : 1024;
     s.min_units = static_cast<int32_t>(std::max<int64_t>(64, 4 * std::min<int64_t>(rows, s.mt)) /
                                        s.kt);
   } else {

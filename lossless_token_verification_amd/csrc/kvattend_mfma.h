@@ -20,21 +20,26 @@
 // relative to their size in both types.
 //
 // K and V units go from the pages straight into LDS (16-byte direct loads, no
-// register stage), NB - 1 units ahead in a ring of NB buffers; rows are permuted
-// by 16-byte vectors (swz_k, swz_v) so that the operand reads of either product
-// spread over all banks.  A row's page comes from the block table NB units
-// before its loads, so that no wait for a table entry drains the ring.
+// register stage), the next unit while one is computed.  Two buffers, and as many
+// workgroups to a CU as registers and LDS then allow, hide start-up and memory
+// latency better than a deeper ring with fewer workgroups (four buffers, head_dim
+// 128, B = 256: single tokens over 500 positions 109 us against 94, windows of 9
+// tokens over 512 to 4096 431 against 427; the other way only where the items just
+// overflow the chip: B = 128 over 2300 positions 211 against 222).  Rows are
+// permuted by 16-byte vectors (swz_k, swz_v) so that the operand reads of either
+// product spread over all banks.  A row's page comes from the block table a unit
+// before its loads, into LDS like them, so that nothing waits for it alone.
 //
 // What bounds it and what it measured (bf16, 32 query and 8 key heads of 128):
 // up to 64 rows the pages' bandwidth (B = 256 verifications of 9 tokens over 512
-// to 4096 positions: 2.60 GB in 432 us, 6.0 TB/s; B = 4 single tokens over 90000
-// to 131071: 2.08 GB in 327 us, 6.4 TB/s; a plain read of such an amount runs at
+// to 4096 positions: 2.60 GB in 422 to 427 us, 6.1 TB/s; B = 4 single tokens over 90000
+// to 131071: 2.08 GB in 319 to 327 us, 6.4 to 6.5 TB/s; a plain read of such an amount runs at
 // 6.9).  With 128 rows the matrix cores and the exponentials in turn, at the
 // clock that the power limit leaves (1.96 GHz): 4 prompts of 2048 to 4096 tokens
 // 332 GF in 385 to 407 us, 815 to 860 TF; 16384 tokens 1000 TF (head_dim 64: 870).
 // Other head sizes cost what the next of the three costs (B = 64, 9 tokens over
-// 2300 positions: 109 us at 80 and 96, 175 us at 192, against 1.09, 1.08 and 2.02
-// ms on the vector units).
+// 2300 positions: 85 us at 80, 87 at 96, 172 at 192, against 1.09, 1.08 and 2.02 ms
+// on the vector units).
 #pragma once
 
 #include <type_traits>
@@ -127,18 +132,18 @@ __device__ __forceinline__ int fresh(int x) {
 }
 
 // RW: query rows per wavefront (16 or 32, the matrix instruction's width), W
-// wavefronts with different rows; units of KT positions in a ring of NB buffers.
+// wavefronts with different rows; units of KT positions, two under way in turn.
 // kPad: head_dim is less than D.
-template <typename T_, int D_, bool kPad_, int RW_, int W_, int KT_, int NB_>
+template <typename T_, int D_, bool kPad_, int RW_, int W_, int KT_>
 struct AttendCfg {
   using T = T_;
   static constexpr bool kPad = kPad_;
-  static constexpr int D = D_, RW = RW_, W = W_, KT = KT_, NB = NB_;
+  static constexpr int D = D_, RW = RW_, W = W_, KT = KT_, NB = 2;
   static constexpr int MT = RW * W;
   static constexpr int NV = D / 8;                 // vectors of a row
   static constexpr int RPL = kWave / NV;           // rows of one direct load
   static constexpr int LOADS = KT / RPL / W;       // of K and of V, per wavefront and unit
-  static constexpr int SUPER = KT * NB;            // positions of a turn of the ring
+  static constexpr int SUPER = KT * NB;            // positions of both buffers, a turn
   static constexpr int IDS = SUPER / kWave;        // table lookups per lane and turn
   static constexpr int QS = RW == 32 ? D / 16 : D / 32;     // steps of the first product
   static constexpr int ST = KT / RW;               // its result tiles
@@ -149,6 +154,7 @@ struct AttendCfg {
   // once (B = 256 verification 511 -> 474 us; at head_dim 256 sequences of many
   // tiles come with 64 rows too, and lose a tenth by them).
   static constexpr bool kOnce = MT <= (D == 256 ? 32 : 64);
+  static constexpr int kPerSimd = D == 64 || (D == 128 && RW == 16) ? 3 : 2;   // wavefronts
   static_assert(KT % (RPL * W) == 0 && KT % 32 == 0 && KT <= kWave && SUPER % kWave == 0,
                 "unit shape");
 };
@@ -164,23 +170,22 @@ __device__ __forceinline__ void load_lds(const void* g, void* l) {
   else __builtin_amdgcn_global_load_lds((gptr_t)g, (lptr_t)l, 16, 0, 0);
 }
 
-// Waits until at most N of the wavefront's vector-memory operations are under
-// way and none of its LDS reads.  The builtin (counts in the hardware's fields:
-// vector memory in bits 0-3 and 14-15, LDS in bits 8-11) is known to the
-// compiler, which then adds no wait of its own for the loads it covers.
-template <int N>
+// Waits until none of the wavefront's vector-memory operations and LDS reads are
+// under way.  The builtin (counts in the hardware's fields: vector memory in bits
+// 0-3 and 14-15, LDS in bits 8-11) is known to the compiler, which then adds no
+// wait of its own for the loads it covers.
 __device__ __forceinline__ void wait_loads() {
   asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | ((N >> 4) << 14));
+  __builtin_amdgcn_s_waitcnt(7 << 4);
   asm volatile("" ::: "memory");
 }
 
-// The bounds name four wavefronts for every W: with the LDS of two workgroups
-// to a CU that is two wavefronts to a SIMD, for which the compiler keeps to 256
-// registers and forms the products in them (given more, it moves every
-// accumulator through the other half of the file in each unit).
+// The bounds name four wavefronts for every W, two or three of them to a SIMD, for
+// which the compiler keeps to 256 or 168 registers and forms the products in them
+// (given more, it moves every accumulator through the other half of the file in
+// each unit).
 template <class C>
-__global__ __launch_bounds__(4 * kWave) __attribute__((amdgpu_waves_per_eu(C::D == 64 ? 3 : 2))) void
+__global__ __launch_bounds__(4 * kWave) __attribute__((amdgpu_waves_per_eu(C::kPerSimd))) void
 attend_mfma_kernel(AttendArgs a) {
   using T = typename C::T;
   constexpr int D = C::D, RW = C::RW, KT = C::KT, NB = C::NB, NV = C::NV, RPL = C::RPL;
@@ -191,9 +196,7 @@ attend_mfma_kernel(AttendArgs a) {
   // not wait for it.
   constexpr int kV = KT * D;   // where the V rows start
   __shared__ __attribute__((aligned(1024))) uint16_t sb0[2 * kV], sb1[2 * kV];
-  __shared__ __attribute__((aligned(1024))) uint16_t sb2[NB > 2 ? 2 * kV : 1];
-  __shared__ __attribute__((aligned(1024))) uint16_t sb3[NB > 3 ? 2 * kV : 1];
-  // looked-up table entries of the ring's next turn, a copy per wavefront
+  // looked-up table entries of the next turn, a copy per wavefront
   __shared__ __attribute__((aligned(256))) int32_t sid[C::W * C::SUPER];
   __shared__ AttendPlanShared<C::W> plan;
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
@@ -507,11 +510,10 @@ attend_mfma_kernel(AttendArgs a) {
   start();
   const int n_units = it.u1 - it.u0;
   if (n_units > 0) {
-    // Step n computes unit n from buffer n % NB while units n + 1 .. n + NB - 1
-    // are under way.  Loads past the last unit read its nearest position again
-    // (one row), which keeps the number of loads under way a constant.  The table
-    // entries of turn q of the ring (units q NB ..) are loaded into LDS as well,
-    // one turn before their use, so that nothing but the counted waits waits.
+    // Step n computes unit n from buffer n % NB while unit n + 1 is under way.
+    // Loads past the last unit read its nearest position again (one row).  The
+    // table entries of turn q (units q NB ..) are loaded into LDS as well, one turn
+    // before their use.
     if (C::kPad) {
       auto clear = [&](uint16_t* sb) {
         for (int i = tid; i < 2 * kV / 8; i += C::W * kWave)
@@ -519,11 +521,9 @@ attend_mfma_kernel(AttendArgs a) {
       };
       clear(sb0);
       clear(sb1);
-      if (NB > 2) clear(sb2);
-      if (NB > 3) clear(sb3);
       __syncthreads();
     }
-    uint16_t* const ring[4] = {sb0, sb1, sb2, sb3};
+    uint16_t* const ring[NB] = {sb0, sb1};
     const int first = it.u0 * KT;
     int32_t* const ids = sid + wave * C::SUPER;
     int64_t off[IDS];
@@ -546,17 +546,17 @@ attend_mfma_kernel(AttendArgs a) {
       load_unit(first + n * KT, off[s * KT / kWave], s * KT % kWave, ring[s]);
     };
     look(0);
-    wait_loads<0>();
+    wait_loads();
     turn(0);
-    wait_loads<0>();                  // the entries are read before the next overwrite them
+    wait_loads();                     // the entries are read before the next overwrite them
     look(1);
 #pragma unroll
     for (int s = 0; s < NB - 1; ++s) load(s, s);
     for (int n = 0; n < n_units; n += NB) {
 #pragma unroll
       for (int s = 0; s < NB; ++s) {
-        wait_loads<(NB - 2) * 2 * C::LOADS>();
-        if (C::W > 1) __builtin_amdgcn_s_barrier();
+        wait_loads();
+        __builtin_amdgcn_s_barrier();
         if (s == 0) {
 #pragma unroll
           for (int i = 0; i < IDS; ++i) mask[i] = mask_next[i];
@@ -569,7 +569,7 @@ attend_mfma_kernel(AttendArgs a) {
       }
     }
     // no load may still be under way when the workgroup gives its LDS back
-    wait_loads<0>();
+    wait_loads();
     // anything not finite: again, a result tile and a unit at a time, carefully
     float z = l * 0.0f;
 #pragma unroll
@@ -583,7 +583,7 @@ attend_mfma_kernel(AttendArgs a) {
         for (int u = it.u0; u < it.u1; ++u) {
           const int page = *entry(u * KT);
           load_unit(u * KT, offset(u * KT, page), 0, sb0);
-          wait_loads<0>();
+          wait_loads();
           __syncthreads();
           compute_careful(sb0, u, paged(page), voff ^ (t * kVTile), x);
           __syncthreads();
@@ -641,23 +641,21 @@ void launch_cfg(const AttendArgs& a, hipStream_t st) {
 }
 
 // Tiles of 32, 64 and 128 rows.  Up to 64 rows the cache's bandwidth bounds the
-// kernel: short units, most of them under way, and 16 rows a wavefront, since
-// more wavefronts start and load a unit faster (32 rows: 36 rows over 500
-// positions at B = 256 130 us against 122; a 16-row tile of one wavefront: single
-// tokens there 126 us against 107, over 1000 positions at B = 1 14.5 against 12.4,
-// over 110000 at B = 4 274 against 282).  128 rows are bound by the matrix and
-// vector units: 32 rows a wavefront and units of 64 positions, half the operand
-// reads and barriers.  Rows of head_dim 256 leave LDS for two buffers and
-// registers for 16 query rows a wavefront, 64 a tile.
+// kernel: short units and 16 rows a wavefront, since more wavefronts start and
+// load a unit faster (with four buffers and head_dim 128, 32 rows a wavefront: 36
+// rows over 500 positions at B = 256 130 us against 122; a 16-row tile of one
+// wavefront: single tokens there 126 us against 107, over 1000 positions at B = 1
+// 14.5 against 12.4, over 110000 at B = 4 274 against 282).  128 rows are bound by
+// the matrix and vector units: 32 rows a wavefront and units of 64 positions, half
+// the operand reads and barriers.  Rows of head_dim 256 leave registers for 16
+// query rows a wavefront, 64 a tile.
 template <typename T, int D, bool kPad>
 hipError_t launch_rows_of(const AttendArgs& a, int mt, hipStream_t st) {
-  constexpr bool kBig = D == 256;
-  constexpr int NB = kBig ? 2 : 4;
   switch (mt) {
-    case 32: launch_cfg<AttendCfg<T, D, kPad, 16, 2, 32, NB>>(a, st); break;
-    case 64: launch_cfg<AttendCfg<T, D, kPad, 16, 4, 32, NB>>(a, st); break;
+    case 32: launch_cfg<AttendCfg<T, D, kPad, 16, 2, 32>>(a, st); break;
+    case 64: launch_cfg<AttendCfg<T, D, kPad, 16, 4, 32>>(a, st); break;
     default:
-      if constexpr (!kBig) launch_cfg<AttendCfg<T, D, kPad, 32, 4, 64, 2>>(a, st);
+      if constexpr (D <= 128) launch_cfg<AttendCfg<T, D, kPad, 32, 4, 64>>(a, st);
       else return hipErrorInvalidValue;
   }
   return hipGetLastError();
