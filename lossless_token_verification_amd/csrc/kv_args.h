@@ -98,7 +98,6 @@ struct SlotInfo {
 
 // Element types, as in the C ABI.
 constexpr int kF32 = 0, kBF16 = 1, kF16 = 2;
-constexpr int kMaxHeadDim = 256;
 // Query rows per tile of the vector-unit kernel, by head size.
 constexpr int kRowsMT64 = 4, kRowsMT128 = 4, kRowsMT256 = 2, kRowsKT = 32;
 

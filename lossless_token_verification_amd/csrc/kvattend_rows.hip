@@ -23,8 +23,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kRowWaves = 4;
 constexpr int kKeysPerStep = 8;
-constexpr int kRowKT = kRowsKT;
-static_assert(kRowWaves * kKeysPerStep == kRowKT, "keys per unit");
+static_assert(kRowWaves * kKeysPerStep == kRowsKT, "keys per unit");
 
 // NF: floats of a row each of the 8 lanes of a key holds (8 * NF >= head_dim).
 template <int NF, int R>
@@ -36,7 +35,7 @@ __global__ __launch_bounds__(kRowWaves * kWave) void attend_rows_kernel(AttendAr
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
   const int x = blockIdx.x / a.kv_heads, h = blockIdx.x - x * a.kv_heads;
   AttendItem it;
-  if (!attend_find<R, kRowKT, kRowWaves>(a, x, a.max_slots > 0 && blockIdx.x == 0, plan, it))
+  if (!attend_find<R, kRowsKT, kRowWaves>(a, x, a.max_slots > 0 && blockIdx.x == 0, plan, it))
     return;
   if (it.splits > 1 && h == 0 && tid == 0) attend_slot_info(a, it);
 
@@ -69,7 +68,7 @@ __global__ __launch_bounds__(kRowWaves * kWave) void attend_rows_kernel(AttendAr
   const int32_t* table = a.table + static_cast<int64_t>(it.b) * a.max_blocks;
   const int64_t head_off = static_cast<int64_t>(h) * a.block_size;
   for (int u = it.u0; u < it.u1; ++u) {
-    const int key = u * kRowKT + wave * kKeysPerStep + kg;
+    const int key = u * kRowsKT + wave * kKeysPerStep + kg;
     bool in = key >= it.key_lo && key < it.key_hi;
     int64_t off = 0;
     if (in) {

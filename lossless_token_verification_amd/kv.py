@@ -20,6 +20,7 @@ MAX_HEAD_DIM = 256
 KV_EXPORTED = ("spec_kv_abi_version", "kv_blocktable_extend", "kv_cache_append",
                "kv_paged_attention_workspace_bytes", "kv_paged_attention")
 
+_I32_MAX = 0x7fffffff
 _CODES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: SV_DTYPE_F16}
 
 
@@ -90,39 +91,44 @@ def _tensor(t, name, dtype, shape, index):
 def _i32(value, name):
     """An argument of the C ABI's 32-bit type (ctypes would cut it to size)."""
     value = int(value)
-    if not -0x80000000 <= value <= 0x7fffffff:
+    if not -_I32_MAX - 1 <= value <= _I32_MAX:
         raise ValueError(f"{name} must be a 32-bit integer, got {value}")
     return value
 
 
-def _caches(k_cache, v_cache, dtype, device):
-    """(blocks, kv_heads, block_size, head_dim, block stride) of a cache pair."""
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
+def _caches(k_cache, v_cache, dtype, index):
+    """(blocks, kv_heads, block_size, head_dim, block stride) of a cache pair on
+    device ``index`` (-1: the host)."""
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must both be [num_blocks, kv_heads, block_size, "
                          "head_dim]")
-    nb, kv, bs, dim = k_cache.shape
-    for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if c.dtype != dtype or c.device != device:
-            raise ValueError(f"{name} must have the rows' dtype ({str(dtype)[6:]}) and device")
-        s = c.stride()
+    nb, kv, bs, dim = shape
+    if k_cache.dtype is not dtype or v_cache.dtype is not dtype or \
+            k_cache.get_device() != index or v_cache.get_device() != index:
+        raise ValueError(f"k_cache and v_cache must have the rows' dtype ({str(dtype)[6:]}) and "
+                         "device")
+    sk, sv = k_cache.stride(), v_cache.stride()
+    for name, s in (("k_cache", sk), ("v_cache", sv)) if sk != sv else (("k_cache", sk),):
         # strides of dimensions of size 1 say nothing
         if (dim > 1 and s[3] != 1) or (bs > 1 and s[2] != dim) or (kv > 1 and s[1] != bs * dim):
             raise ValueError(f"{name}: each block must be contiguous")
     if nb <= 1:
         return nb, kv, bs, dim, 0
-    stride = k_cache.stride(0)
-    if stride != v_cache.stride(0):
+    if sk[0] != sv[0]:
         raise ValueError("k_cache and v_cache must have one block stride")
-    if stride < kv * bs * dim:                  # (an expanded cache has 0)
+    if sk[0] < kv * bs * dim:                   # (an expanded cache has 0)
         raise ValueError("the blocks of a cache must not overlap")
-    return _i32(nb, "num_blocks"), kv, bs, dim, stride
+    return nb, kv, bs, dim, sk[0]
 
 
 def _row_stride(t, name):
     """Elements between the token rows of [T, heads, dim] with contiguous heads
     (0: a single row leaves it open)."""
-    T, heads, dim = t.shape
     s = t.stride()
+    if len(s) != 3:
+        raise ValueError(f"{name} must be [T, heads, head_dim]")
+    T, heads, dim = t.shape
     if (dim > 1 and s[2] != 1) or (heads > 1 and s[1] != dim):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
     if T <= 1:
@@ -190,31 +196,41 @@ def kv_cache_append(k, v, slot_map, k_cache, v_cache):
     head_dim] in place.  ``slot_map`` [T] int64: negative or out-of-cache slots
     skip their row; the others must differ.  Float32, bfloat16 or float16."""
     lib = _pkg.library()
-    if k.dtype not in _CODES:
+    code = _CODES.get(k.dtype)
+    if code is None:
         raise TypeError(f"k must be float32, bfloat16 or float16, got {k.dtype}")
     dev = _gpu(k)
-    nb, kv, bs, dim, block_stride = _caches(k_cache, v_cache, k.dtype, k.device)
-    if k.dim() != 3 or k.shape[1:] != (kv, dim) or v.shape != k.shape or v.dtype != k.dtype or \
+    nb, kv, bs, dim, block_stride = _caches(k_cache, v_cache, k.dtype, dev)
+    shape = k.shape
+    if shape[1:] != (kv, dim) or v.shape != shape or v.dtype is not k.dtype or \
             v.get_device() != dev:
         raise ValueError(f"k and v must be [T, {kv}, {dim}] of one dtype on one device")
-    T = _i32(k.shape[0], "T")
-    desc = AppendDesc(T, kv, dim, bs, nb, _CODES[k.dtype], _row_stride(k, "k"),
-                      _row_stride(v, "v"), block_stride)
+    T = shape[0]
+    if max(T, nb) > _I32_MAX:
+        raise ValueError(f"T and num_blocks must be 32-bit integers, got {T} and {nb}")
+    desc = AppendDesc(T, kv, dim, bs, nb, code, _row_stride(k, "k"), _row_stride(v, "v"),
+                      block_stride)
     _call(lib.kv_cache_append, dev, ctypes.byref(desc), k.data_ptr(), v.data_ptr(),
           _tensor(slot_map, "slot_map", torch.int64, (T,), dev), k_cache.data_ptr(),
           v_cache.data_ptr())
 
 
 def _attention_desc(q, k_cache, v_cache, block_table, scale, sliding_window, max_new):
-    if q.dtype not in _CODES:
+    code = _CODES.get(q.dtype)
+    if code is None:
         raise TypeError(f"q must be float32, bfloat16 or float16, got {q.dtype}")
-    nb, kv, bs, dim, block_stride = _caches(k_cache, v_cache, q.dtype, q.device)
-    if q.dim() != 3 or q.shape[2] != dim:
+    nb, kv, bs, dim, block_stride = _caches(k_cache, v_cache, q.dtype, q.get_device())
+    stride = _row_stride(q, "q")
+    T, heads, q_dim = q.shape
+    if q_dim != dim:
         raise ValueError(f"q must be [T, heads, {dim}]")
     B, width = block_table.shape
-    return AttentionDesc(B, _i32(q.shape[0], "T"), q.shape[1], kv, dim, bs, nb, width,
-                         _CODES[q.dtype], _i32(sliding_window, "sliding_window"),
-                         _i32(max_new, "max_new"), 0, _row_stride(q, "q"), block_stride,
+    if max(T, nb, sliding_window, max_new) > _I32_MAX or min(sliding_window, max_new) < 0:
+        for name, value in (("T", T), ("num_blocks", nb), ("sliding_window", sliding_window),
+                            ("max_new", max_new)):
+            _i32(value, name)
+    return AttentionDesc(B, T, heads, kv, dim, bs, nb, width, code, int(sliding_window),
+                         int(max_new), 0, stride, block_stride,
                          dim ** -0.5 if scale is None else float(scale), 0.0)
 
 

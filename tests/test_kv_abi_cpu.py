@@ -229,7 +229,7 @@ def test_binding_refuses_overlapping_rows_and_blocks(sv):
         sv.kv._row_stride(row.expand(3, 4, 64), "k")
     # one row has no stride to speak of
     assert sv.kv._row_stride(row, "k") == 0
-    assert sv.kv._caches(wide[:1], wide[:1], torch.bfloat16, wide.device)[4] == 0
+    assert sv.kv._caches(wide[:1], wide[:1], torch.bfloat16, -1)[4] == 0
 
 
 @pytest.mark.parametrize("name", ["sliding_window", "max_new"])
