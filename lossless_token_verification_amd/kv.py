@@ -3,7 +3,8 @@
 
 As in the package's other calls, tensors are checked for device, dtype, shape
 and layout, and their pointers go to the C ABI on torch's current stream of
-their device; every call is asynchronous.
+their device; every call is asynchronous.  Inference only: no call records a
+gradient.
 """
 
 import ctypes
