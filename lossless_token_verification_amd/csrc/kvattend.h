@@ -89,9 +89,11 @@ __device__ __forceinline__ bool attend_find(const AttendArgs& a, int x, bool cou
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
   if (tid < kLengthClasses) sh.cls[tid] = 0;
   if (tid == 0) sh.found = 0;
+  // Sums over the sequences, the same in every thread (the branches on them below
+  // hold barriers): reduced, or, of one sequence, made by each thread for itself.
   uint64_t units = 0, tiles = 0;
   int longest = 0;
-  for (int b = tid; b < a.B; b += NT) {
+  for (int b = a.B > 1 ? tid : 0; b < a.B; b += NT) {
     const AttendSeq s = attend_seq<MT, KT>(a, b);
     tiles += s.tiles;
     units += static_cast<uint64_t>(s.tiles) * s.units;
@@ -136,7 +138,9 @@ __device__ __forceinline__ bool attend_find(const AttendArgs& a, int x, bool cou
                          (a.want_items + 1) / 2);
     S = share(a.want_items);      // if the splits round up to few enough items
     uint64_t items = tiles;
-    if (tiles <= static_cast<uint64_t>(a.want_items)) {
+    if (tiles <= static_cast<uint64_t>(a.want_items) && a.B == 1) {
+      items = tiles * max((static_cast<uint32_t>(longest) + S - 1) / S, 1u);
+    } else if (tiles <= static_cast<uint64_t>(a.want_items)) {
       items = 0;
       for (int b = tid; b < a.B; b += NT) {
         const AttendSeq s = attend_seq<MT, KT>(a, b);
