@@ -174,8 +174,10 @@ size_t kv_paged_attention_workspace_bytes(const spec_kv_attention_desc* desc);
  *               may be NULL if that is 0
  * q and the caches need 16-byte aligned pointers and strides (out: pointer).
  * Scores, softmax sums and the output are accumulated in float32; bf16 and f16
- * round the softmax weights to that type for the matrix cores.  The same call
- * on the same data gives the same bits. */
+ * round the softmax weights to that type for the matrix cores (half a step of
+ * the type relative to a weight; in f16 also up to 2^-32 of the largest weight
+ * where that is more), not their sum.  The same call on the same data gives the
+ * same bits. */
 int32_t kv_paged_attention(const spec_kv_attention_desc* desc, const void* q,
                            const void* k_cache, const void* v_cache,
                            const int32_t* block_table, const int32_t* seq_lens,

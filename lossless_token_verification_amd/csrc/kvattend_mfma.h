@@ -14,10 +14,16 @@
 // the positions that a result register quadruple holds are taken as that
 // operand's k order, and V is read in the same order.
 //
-// Softmax in one pass: the maximum m moves only when a score exceeds it by
-// more than kSlack (log2 units), so the accumulators are rescaled in the first
-// unit and hardly ever after; weights stay below 2^kSlack, exactly represented
-// relative to their size in both types.
+// Softmax in one pass: weights are 2^(score - m) in log2 units, and m moves, to
+// kShift below the largest score, only when a score exceeds that by more than
+// kSlack, so the accumulators are rescaled in the first unit and hardly ever
+// after.  The weights are rounded to the type for the second product (half a
+// step, 2^-8 of a weight in bf16, 2^-11 in f16: a choice that keeps both products
+// at the 16-bit rate); their sum is taken before the rounding, in float32.  f16
+// has 5 exponent bits: at kShift = 7 weights reach 2^15, those of 2^-21 of the
+// largest and more keep all their bits, smaller ones lose up to 2^-32 of it each
+// (131072 keys far below one dominant key: 2^-15 of the output, against f16's
+// own 2^-11; with kShift = 0 the whole share of such keys, 0.4 % of the output).
 //
 // K and V units go from the pages straight into LDS (16-byte direct loads, no
 // register stage), the next unit while one is computed.  Two buffers, and as many
@@ -59,6 +65,7 @@ struct Mma;
 template <>
 struct Mma<__bf16> {
   static constexpr uint32_t kExp = 0x7f80u;   // exponent bits: all set = not finite
+  static constexpr float kShift = 0.0f;       // log2 of the largest weight where m moves
   __device__ static f32x16 mma32(u32x4 a, u32x4 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
@@ -71,6 +78,7 @@ struct Mma<__bf16> {
 template <>
 struct Mma<_Float16> {
   static constexpr uint32_t kExp = 0x7c00u;
+  static constexpr float kShift = 7.0f;
   __device__ static f32x16 mma32(u32x4 a, u32x4 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
                                                   __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
@@ -375,9 +383,10 @@ attend_mfma_kernel(AttendArgs a) {
       for (int r = 0; r < SR; ++r) mx = fmaxf(mx, st[t][r]);
     if (RW == 16) mx = max_across<16>(mx);
     mx = max_across<32>(mx);
-    const bool move = mx * c > m + kSlack;      // m = -inf: any score moves it
+    constexpr float kShift = Mma<T>::kShift;
+    const bool move = mx * c > m + (kSlack + kShift);      // m = -inf: any score moves it
     if (__any(move)) {
-      const float mn = move ? mx * c : m;
+      const float mn = move ? mx * c - kShift : m;
       const float f = __builtin_amdgcn_exp2f(m - (mn == -INFINITY ? 0.0f : mn));
       m = mn;
       l *= f;

@@ -1,9 +1,11 @@
 """GPU parity of kv_paged_attention at calls that its other tests leave out, within
-bounds by arithmetic (tests/kvcases.py)."""
+bounds by arithmetic (tests/kvcases.py, tests/kvbounds.py)."""
 
+import numpy as np
 import pytest
 import torch
 
+from tests import kvbounds as B
 from tests import kvcases as C
 
 pytestmark = pytest.mark.gpu
@@ -37,3 +39,35 @@ def test_one_sequence_of_more_tiles_than_places(sv, ctx, new, heads, dim, dtype,
     torch.cuda.synchronize()
     assert r["workspace"] is not None
     C.check(C.to64(r["out"]), C.to64(r["lse"]), C.reference(case), dtype, dim)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("gap", [12.75, 16.90625, 17.40625])
+@pytest.mark.parametrize("dim,heads,kv", [(64, 32, 8), (128, 16, 4), (256, 8, 8)])
+def test_flat_tail_behind_a_dominant_key(sv, dtype, gap, dim, heads, kv):
+    """Every key but the first scores ``gap`` (in the type) below it (18.4 to 25.1 in log2 units):
+    the output is the tail's share, p w / (1 + p w) at position p, w = exp(-gap)."""
+    T, bs = 4096 if dtype != "f32" else 700, 16
+    dt = C.DT[dtype]
+    g = torch.Generator().manual_seed(int(gap * 32) + dim)
+    table = torch.randperm(T // bs + 1, generator=g).to(torch.int32)[None].to(C.DEV)
+    k = torch.zeros((T // bs + 1, kv, bs, dim), dtype=dt, device=C.DEV)
+    v = torch.ones_like(k)
+    k[table[0, 0].item(), :, 0, 1] = gap
+    gap = float(k[table[0, 0].item(), 0, 0, 1])     # as the type holds it
+    v[table[0, 0].item(), :, 0] = 0.0
+    q = torch.zeros((T, heads, dim), dtype=dt, device=C.DEV)
+    q[:, :, 1] = 1.0
+    r = sv.kv_paged_attention(q, k, v, table, torch.tensor([T], dtype=torch.int32, device=C.DEV),
+                              torch.tensor([0, T], dtype=torch.int32, device=C.DEV), scale=1.0,
+                              lse=True, max_new=T)
+    torch.cuda.synchronize()
+    p = np.arange(T)[:, None]
+    tail = np.broadcast_to(p * np.exp(-gap), (T, heads))
+    ref = dict(out=np.broadcast_to((tail / (1 + tail))[..., None], (T, heads, dim)),
+               lse=gap + np.log1p(tail), keys=np.broadcast_to(p + 1.0, (T, heads)),
+               v_max=np.ones((T, heads)), score_abs=np.full((T, heads), gap),
+               score_top=np.full((T, heads), gap))
+    ref["weight_abs"] = ref["out"]
+    share = B.check(C.to64(r["out"]), C.to64(r["lse"]), ref, dtype, dim)
+    print(f"{share:.3f} of the bound")
