@@ -19,7 +19,9 @@
 // kSlack, so the accumulators are rescaled in the first unit and hardly ever
 // after.  The weights are rounded to the type for the second product (half a
 // step, 2^-8 of a weight in bf16, 2^-11 in f16: a choice that keeps both products
-// at the 16-bit rate); their sum is taken before the rounding, in float32.  f16
+// at the 16-bit rate); their sum is taken before the rounding, in float32.  bf16
+// has float32's exponents: kShift = -kSlack keeps weights at 1 and less, so that
+// no sum of values overflows that would not with the exact maximum.  f16
 // has 5 exponent bits: at kShift = 7 weights reach 2^15, those of 2^-21 of the
 // largest and more keep all their bits, smaller ones lose up to 2^-32 of it each
 // (131072 keys far below one dominant key: 2^-15 of the output, against f16's
@@ -60,12 +62,14 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
+constexpr float kSlack = 8.0f;   // log2 units that a weight may grow before m moves
+
 template <typename T>
 struct Mma;
 template <>
 struct Mma<__bf16> {
   static constexpr uint32_t kExp = 0x7f80u;   // exponent bits: all set = not finite
-  static constexpr float kShift = 0.0f;       // log2 of the largest weight where m moves
+  static constexpr float kShift = -kSlack;    // log2 of the largest weight where m moves
   __device__ static f32x16 mma32(u32x4 a, u32x4 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
@@ -166,8 +170,6 @@ struct AttendCfg {
   static_assert(KT % (RPL * W) == 0 && KT % 32 == 0 && KT <= kWave && SUPER % kWave == 0,
                 "unit shape");
 };
-
-constexpr float kSlack = 8.0f;
 
 typedef const void __attribute__((address_space(1)))* gptr_t;
 typedef void __attribute__((address_space(3)))* lptr_t;

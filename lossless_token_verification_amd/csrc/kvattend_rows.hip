@@ -4,9 +4,11 @@
 // One workgroup takes a few query rows and a split of their keys; its
 // wavefronts take 8 keys a step each, 8 lanes to a key, so that a key's row is
 // read in whole 128-byte lines and a dot product needs three exchanges.
-// Softmax in one pass: every group of 8 lanes keeps its own running maximum m
-// and sum l and the output relative to it; a new maximum scales both by
-// 2^(m_old - m_new).  The groups' states are merged once at the end.
+// Softmax in one pass: every group of 8 lanes keeps its own reference m, kLead
+// above the largest score so far (log2 units), and the sum l and the output
+// relative to it; a new one scales both by 2^(m_old - m_new).  The groups' states
+// are merged once at the end.  Weights are 2^-kLead at most, so that 256 of the
+// largest values add up without overflow.
 //
 // Single tokens are bound by the pages' bandwidth (B = 64 over 2300 positions, 32
 // query and 8 key heads of 128: 1.2 GB in 240 us, 5.0 TB/s), more rows by the
@@ -23,6 +25,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kRowWaves = 4;
 constexpr int kKeysPerStep = 8;
+constexpr float kLead = 8.0f;
 static_assert(kRowWaves * kKeysPerStep == kRowsKT, "keys per unit");
 
 // NF: floats of a row each of the 8 lanes of a key holds (8 * NF >= head_dim).
@@ -108,9 +111,9 @@ __global__ __launch_bounds__(kRowWaves * kWave) void attend_rows_kernel(AttendAr
       if (!in || key > pos[r] ||
           (a.window > 0 && static_cast<int64_t>(key) <= static_cast<int64_t>(pos[r]) - a.window))
         continue;
-      const float t = s[r] * c;
-      const float mn = fmaxf(m[r], t), ref = mn == -INFINITY ? 0.0f : mn;
-      const float f = __builtin_amdgcn_exp2f(m[r] - ref), p = __builtin_amdgcn_exp2f(t - ref);
+      const float mn = fmaxf(m[r], fmaf(s[r], c, kLead)), ref = mn == -INFINITY ? 0.0f : mn;
+      const float f = __builtin_amdgcn_exp2f(m[r] - ref);
+      const float p = __builtin_amdgcn_exp2f(fmaf(s[r], c, -ref));
       m[r] = mn;
       l[r] = fmaf(l[r], f, p);
 #pragma unroll

@@ -71,3 +71,25 @@ def test_flat_tail_behind_a_dominant_key(sv, dtype, gap, dim, heads, kv):
     ref["weight_abs"] = ref["out"]
     share = B.check(C.to64(r["out"]), C.to64(r["lse"]), ref, dtype, dim)
     print(f"{share:.3f} of the bound")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("ctx,new", [([100], [1]), ([6000, 40], [2, 40])])
+def test_values_near_the_largest(sv, dtype, dim, ctx, new):
+    """Values of 4e36: a late key that outweighs the ones before it by 2^7.5 leaves the
+    sums finite."""
+    case = C.attend_case(ctx, new, 2, 1, dim, 16, dtype, seed=33)
+    case["q"].zero_()
+    case["q"][:, :, 0] = 1.0
+    for b, L in enumerate(case["seq_lens"].tolist()):
+        pos = torch.arange(L)
+        page, at = case["block_table"][b, pos // 16].long(), pos % 16
+        case["k_cache"][page, 0, at] = 0.0
+        last = (ctx[b] - 1) // 16, (ctx[b] - 1) % 16
+        case["k_cache"][case["block_table"][b, last[0]].long(), 0, last[1], 0] = 5.1875
+        case["v_cache"][page, 0, at] *= 4e36
+    g = C.on_gpu(case)
+    r = sv.kv_paged_attention(*[g[n] for n in NAMES], scale=1.0, lse=True)
+    torch.cuda.synchronize()
+    B.check(C.to64(r["out"]), C.to64(r["lse"]), C.reference(case, 1.0), dtype, dim)
