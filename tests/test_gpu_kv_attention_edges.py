@@ -93,3 +93,30 @@ def test_values_near_the_largest(sv, dtype, dim, ctx, new):
     r = sv.kv_paged_attention(*[g[n] for n in NAMES], scale=1.0, lse=True)
     torch.cuda.synchronize()
     B.check(C.to64(r["out"]), C.to64(r["lse"]), C.reference(case, 1.0), dtype, dim)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("dim", [64, 128, 256, 72])
+@pytest.mark.parametrize("new", [1, 3, 40])
+def test_long_contexts(sv, dtype, dim, new):
+    """Split keys and their joining within bounds that are sharp over long contexts."""
+    ctx = [2500, 10] if new == 40 and dim > 64 else [9001, 10, 4000]
+    case = C.attend_case(ctx, [new] * len(ctx), 2, 1, dim, 16, dtype, seed=50 + new)
+    g = C.on_gpu(case)
+    r = sv.kv_paged_attention(*[g[n] for n in NAMES], lse=True)
+    torch.cuda.synchronize()
+    share = B.check(C.to64(r["out"]), C.to64(r["lse"]), C.reference(case), dtype, dim)
+    print(f"{share:.3f} of the bound")
+
+
+@pytest.mark.parametrize("dim", [8, 24, 40, 56, 72, 80, 96, 120, 136, 160, 192, 248])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_long_contexts_of_head_sizes_between(sv, dtype, dim):
+    for i, (ctx, new, heads, kv, bs, window) in enumerate([
+            ([3000, 5], [1, 1], 4, 2, 16, 0), ([70, 400], [9, 20], 2, 2, 24, 0),
+            ([10, 700], [150, 60], 4, 2, 32, 0), ([2500], [130], 2, 1, 16, 0)]):
+        case = C.attend_case(ctx, new, heads, kv, dim, bs, dtype, seed=60 + i)
+        g = C.on_gpu(case)
+        r = sv.kv_paged_attention(*[g[n] for n in NAMES], lse=True, max_new=max(new))
+        torch.cuda.synchronize()
+        B.check(C.to64(r["out"]), C.to64(r["lse"]), C.reference(case), dtype, dim, (i, dim))
