@@ -255,8 +255,10 @@ def kv_paged_attention(q, k_cache, v_cache, block_table, seq_lens, cu_tokens, *,
     ``max_new``, the most new tokens of a sequence (0: the batch's mean is taken),
     picks the tile shape only.  Returns dict(out [T, heads, head_dim], lse
     [T, heads] float32 or None, workspace).  ``out``: a dict of an earlier call of
-    the same shape, whose tensors are reused.  Rows of no sequence are left as
-    they were."""
+    the same shape, whose tensors are reused; a call with another ``max_new`` or
+    ``sliding_window`` that needs a larger workspace puts one there.  An explicit
+    ``workspace`` has to be large enough.  Rows of no sequence are left as they
+    were."""
     lib = _pkg.library()
     desc = _attention_desc(q, k_cache, v_cache, block_table, scale, sliding_window, max_new)
     dev = _gpu(q)
@@ -270,7 +272,8 @@ def kv_paged_attention(q, k_cache, v_cache, block_table, seq_lens, cu_tokens, *,
                    if lse else None, workspace=None)
     elif lse and out["lse"] is None:
         raise ValueError("out holds no lse tensor")
-    if workspace is None:
+    kept = workspace is None      # out's own, which another hint or window may have sized
+    if kept:
         workspace = out["workspace"]
     if workspace is None:
         need = lib.kv_paged_attention_workspace_bytes(ctypes.byref(desc))
@@ -279,11 +282,21 @@ def kv_paged_attention(q, k_cache, v_cache, block_table, seq_lens, cu_tokens, *,
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on q's device")
     out["workspace"] = workspace
-    _call(lib.kv_paged_attention, dev, ctypes.byref(desc), q.data_ptr(), k_cache.data_ptr(),
-          v_cache.data_ptr(), pt, pl, pc,
-          _tensor(out["out"], "out", q.dtype, (T, heads, dim), dev),
-          _tensor(out["lse"], "out lse", torch.float32, (T, heads), dev)
-          if out["lse"] is not None else None,
-          workspace.data_ptr() if workspace is not None else None,
-          workspace.numel() * workspace.element_size() if workspace is not None else 0)
+    tensors = (ctypes.byref(desc), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), pt, pl, pc,
+               _tensor(out["out"], "out", q.dtype, (T, heads, dim), dev),
+               _tensor(out["lse"], "out lse", torch.float32, (T, heads), dev)
+               if out["lse"] is not None else None)
+    try:
+        _call(lib.kv_paged_attention, dev, *tensors,
+              workspace.data_ptr() if workspace is not None else None,
+              workspace.numel() * workspace.element_size() if workspace is not None else 0)
+    except _pkg.SpecVerifyError as e:
+        if not kept or e.status != _pkg.SV_ERR_WORKSPACE:
+            raise
+        # a larger one takes its place and keeps it: a captured call may still use it
+        need = lib.kv_paged_attention_workspace_bytes(ctypes.byref(desc))
+        larger = torch.empty(need, dtype=torch.uint8, device=q.device)
+        larger.replaces = workspace
+        out["workspace"] = larger
+        _call(lib.kv_paged_attention, dev, *tensors, larger.data_ptr(), need)
     return out

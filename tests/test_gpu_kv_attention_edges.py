@@ -120,3 +120,42 @@ def test_long_contexts_of_head_sizes_between(sv, dtype, dim):
         r = sv.kv_paged_attention(*[g[n] for n in NAMES], lse=True, max_new=max(new))
         torch.cuda.synchronize()
         B.check(C.to64(r["out"]), C.to64(r["lse"]), C.reference(case), dtype, dim, (i, dim))
+
+
+def test_reused_outputs_take_any_hint_and_window(sv):
+    """One out dict over calls whose hint and window ask for larger workspaces, in any
+    order; a call captured with the first workspace still replays right."""
+    case = C.attend_case([9000, 5000, 40, 7], [10, 10, 10, 10], 32, 8, 128, 16, "bf16", seed=34)
+    g = C.on_gpu(case)
+    args = [g[n] for n in NAMES]
+    out = sv.kv_paged_attention(*args, max_new=1)
+    first = out["workspace"]
+    alone = out["out"].clone()
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(stream):
+        with torch.cuda.graph(graph, stream=stream):
+            sv.kv_paged_attention(*args, max_new=1, out=out)
+    del first
+    grown = set()
+    for hint, window in ((1, 0), (9, 0), (40, 0), (1, 512), (9, 512), (40, 300), (0, 0), (9, 0)):
+        fresh = sv.kv_paged_attention(*args, max_new=hint, sliding_window=window)
+        r = sv.kv_paged_attention(*args, max_new=hint, sliding_window=window, out=out)
+        torch.cuda.synchronize()
+        assert r is out and torch.equal(r["out"], fresh["out"]), (hint, window)
+        grown.add(r["workspace"].numel())
+        # memory that the allocator hands out again is not the captured call's
+        junk = [torch.full((n,), 0x7f, dtype=torch.uint8, device=C.DEV) for n in sorted(grown)]
+        out["out"].fill_(1.0)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out["out"], alone), (hint, window)
+        assert all((j == 0x7f).all() for j in junk)
+        del junk
+    assert len(grown) > 1
+    # an explicit workspace is the caller's
+    small = torch.empty(min(grown) - 256, dtype=torch.uint8, device=C.DEV)
+    with pytest.raises(sv.SpecVerifyError, match="workspace has"):
+        sv.kv_paged_attention(*args, max_new=1, out=out, workspace=small)
