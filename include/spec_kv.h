@@ -46,6 +46,9 @@ extern "C" {
 
 #define SV_DTYPE_F16 2        /* float16, caches and attention only              */
 #define SV_MAX_HEAD_DIM 256   /* head_dim of kv_paged_attention                  */
+#define SV_MAX_ATTEND_BATCH 65536   /* sequences of kv_paged_attention; its work split
+                                       costs every workgroup a pass over the batch
+                                       (a tenth of the time at some 2000 sequences) */
 
 int32_t spec_kv_abi_version(void);
 
@@ -123,7 +126,7 @@ int32_t kv_cache_append(const spec_kv_append_desc* desc, const void* k, const vo
                         void* hip_stream);
 
 typedef struct {
-  int32_t batch;          /* B in [0, 2^24]                                      */
+  int32_t batch;          /* B in [0, SV_MAX_ATTEND_BATCH]                       */
   int32_t tokens;         /* T >= 0 query rows; T * heads < 2^31                 */
   int32_t heads;          /* query heads, a multiple of kv_heads                 */
   int32_t kv_heads;       /* >= 1; head h reads key head h / (heads / kv_heads)   */

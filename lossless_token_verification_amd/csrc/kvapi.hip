@@ -46,7 +46,11 @@ int32_t check_ptr(const void* p, bool required, uintptr_t align, const char* nam
 constexpr int32_t kMaxHeads = 1 << 16;
 constexpr int32_t kMaxRowDim = 1 << 12;   // head_dim of a cache append
 constexpr int64_t kMaxStride = int64_t{1} << 40;
-constexpr int32_t kMaxBatch = 1 << 24;
+constexpr int32_t kMaxBatch = 1 << 24;    // sequences of an extension
+// Sequences of an attention call: every workgroup passes over all of them to find
+// its share, so the time has a part that grows with the square (single tokens over
+// 100 positions: B = 1024 0.18 ms, 4096 1.5, 16384 19, 32768 72).
+constexpr int32_t kMaxAttendBatch = SV_MAX_ATTEND_BATCH;
 constexpr int32_t kMaxRows = 1 << 30;     // rows of an extension's token arrays
 constexpr int64_t kMaxWorkgroups = int64_t{1} << 24;
 
@@ -134,7 +138,7 @@ int32_t make_attend_plan(const spec_kv_attention_desc* d, AttendPlan* p) {
   if (d->reserved != 0 || d->reserved_f != 0.0f)
     return fail(SV_ERR_INVALID_ARG, "reserved fields must be 0");
   if (d->batch < 0) return fail(SV_ERR_INVALID_ARG, "batch < 0");
-  if (d->batch > kMaxBatch) return fail(SV_ERR_UNSUPPORTED, "batch > %d", kMaxBatch);
+  if (d->batch > kMaxAttendBatch) return fail(SV_ERR_UNSUPPORTED, "batch > %d", kMaxAttendBatch);
   if (d->tokens < 0) return fail(SV_ERR_INVALID_ARG, "tokens < 0");
   if (d->max_blocks < 0) return fail(SV_ERR_INVALID_ARG, "max_blocks < 0");
   if (d->sliding_window < 0) return fail(SV_ERR_INVALID_ARG, "sliding_window < 0");

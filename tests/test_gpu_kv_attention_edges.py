@@ -159,3 +159,16 @@ def test_reused_outputs_take_any_hint_and_window(sv):
     small = torch.empty(min(grown) - 256, dtype=torch.uint8, device=C.DEV)
     with pytest.raises(sv.SpecVerifyError, match="workspace has"):
         sv.kv_paged_attention(*args, max_new=1, out=out, workspace=small)
+
+
+@pytest.mark.parametrize("dtype,dim", [("bf16", 64), ("f16", 128), ("f32", 64)])
+def test_batches_of_thousands(sv, dtype, dim):
+    """Single tokens and short windows of 5000 sequences, one long one among them."""
+    rng = np.random.default_rng(35)
+    ctx, new = rng.integers(0, 30, 5000).tolist(), rng.integers(0, 3, 5000).tolist()
+    ctx[4321], new[4321] = 3000, 2
+    case = C.attend_case(ctx, new, 2, 1, dim, 16, dtype, seed=35)
+    g = C.on_gpu(case)
+    r = sv.kv_paged_attention(*[g[n] for n in NAMES], lse=True, max_new=2)
+    torch.cuda.synchronize()
+    B.check(C.to64(r["out"]), C.to64(r["lse"]), C.reference(case), dtype, dim)
