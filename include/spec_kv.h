@@ -59,10 +59,12 @@ int32_t spec_kv_abi_version(void);
  * The pool is a stack: free_blocks[0 .. *free_count), popped from its end.
  * First the blocks freed[b, 0 .. num_freed[b]) of every sequence in order
  * (freed_blocks / num_freed as kv_blocktable_truncate leaves them; a num_freed
- * of -1 adds none) are pushed, as far as free_capacity reaches.  Then the
- * sequences take theirs in order, ascending in logical blocks.  When the pool
- * runs short, the first sequence that it cannot serve and every later one that
- * needs a block get none.
+ * of -1 adds none) are pushed.  Ids that free_capacity has no room for are
+ * dropped, in no list from then on: free_count + the ids given back - the blocks
+ * taken (num_taken) - free_left is how many; a stack with room for every block of
+ * the cache drops none.  Then the sequences take theirs in order, ascending in
+ * logical blocks.  When the pool runs short, the first sequence that it cannot
+ * serve and every later one that needs a block get none.
  *
  *   block_table  [B, max_blocks] device int32, in/out: only new entries written
  *   seq_lens     [B]  device int32, read

@@ -145,7 +145,8 @@ def kv_blocktable_extend(block_table, seq_lens, num_new, free_blocks, free_count
 
     Takes ids from the end of the stack ``free_blocks[:free_count]`` (after
     pushing ``freed_blocks`` [B, max_freed] / ``num_freed`` [B] as
-    ``kv_blocktable_truncate`` returns them), writes them to ``block_table``
+    ``kv_blocktable_truncate`` returns them; ids that ``free_blocks`` has no room
+    for are dropped, so give it room for every block of the cache), writes them to ``block_table``
     [B, max_blocks] in place, and returns a dict of device tensors: new_lens
     [B], num_taken [B] (-1: bad request, -2: pool short; such sequences stay
     as they were), free_left [1], cu_tokens [B+1], slot_map [max_tokens] int64
