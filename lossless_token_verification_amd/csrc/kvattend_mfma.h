@@ -484,7 +484,8 @@ attend_mfma_kernel(AttendArgs a) {
           *reinterpret_cast<f32x4*>(po + r * 2) = f32x4{x[r], x[r + 1], x[r + 2], x[r + 3]};
       return;
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const float inv = 1.0f / l;
+    auto y = [&](int r) { return l == 0.0f ? 0.0f : x[r] * inv; };   // (x may be NaN there)
     int token, head;
     attend_row(a, it.token0, it.row0 + fresh(row), h, token, head);
     const int e = t * RW + 4 * hi_lane;
@@ -494,7 +495,7 @@ attend_mfma_kernel(AttendArgs a) {
       if (C::kPad && e + r * 2 >= dim) continue;
       typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
       *reinterpret_cast<u32x2*>(po + r * 2) =
-          u32x2{pack2<T>(x[r] * inv, x[r + 1] * inv), pack2<T>(x[r + 2] * inv, x[r + 3] * inv)};
+          u32x2{pack2<T>(y(r), y(r + 1)), pack2<T>(y(r + 2), y(r + 3))};
     }
   };
   auto store_sums = [&]() {

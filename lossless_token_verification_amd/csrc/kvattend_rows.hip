@@ -241,11 +241,11 @@ __global__ __launch_bounds__(kRowWaves * kWave) void attend_join_kernel(AttendAr
       int token, head;
       attend_row(a, s.token0, s.row0 + r, h, token, head);
       const int64_t at = static_cast<int64_t>(token) * a.heads + head;
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      const float inv = 1.0f / l;
       typedef T t4 __attribute__((ext_vector_type(4)));
       t4 y;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) y[e] = static_cast<T>(o[e] * inv);
+      for (int e = 0; e < 4; ++e) y[e] = static_cast<T>(l == 0.0f ? 0.0f : o[e] * inv);
       *reinterpret_cast<t4*>(static_cast<T*>(a.out) + at * a.D + d) = y;
       if (a.lse && d == 0) a.lse[at] = l == 0.0f ? -INFINITY : (mx + log2f(l)) * kLn2;
     }

@@ -172,3 +172,30 @@ def test_batches_of_thousands(sv, dtype, dim):
     r = sv.kv_paged_attention(*[g[n] for n in NAMES], lse=True, max_new=2)
     torch.cuda.synchronize()
     B.check(C.to64(r["out"]), C.to64(r["lse"]), C.reference(case), dtype, dim)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("dim", [64, 80, 128, 256])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_scores_of_minus_infinity_alone_give_zero(sv, dtype, dim, bad):
+    """Whatever the values there hold, with split keys and without."""
+    for ctx, new in (([40, 6000, 30], [3, 1, 20]), ([300], [70])):
+        case = C.attend_case(ctx, new, 2, 1, dim, 16, dtype, seed=37)
+        case["q"].zero_()
+        case["q"][:, :, 3] = 1.0
+        L = int(case["seq_lens"][-1 if len(ctx) == 1 else 1])
+        b = len(ctx) // 2
+        pos = torch.arange(L)
+        page = case["block_table"][b, pos // 16].long()
+        case["k_cache"][page, 0, pos % 16, 3] = float("-inf")
+        clean = {**case, "k_cache": case["k_cache"].clone(), "v_cache": case["v_cache"].clone()}
+        clean["k_cache"][page, 0, pos % 16, 3] = 0.0
+        case["v_cache"][page[::7], 0, pos[::7] % 16, 1] = bad
+        g = C.on_gpu(case)
+        r = sv.kv_paged_attention(*[g[n] for n in NAMES], lse=True)
+        torch.cuda.synchronize()
+        rows = slice(int(case["cu_tokens"][b]), int(case["cu_tokens"][b + 1]))
+        assert (r["out"][rows] == 0).all() and torch.isneginf(r["lse"][rows]).all(), (ctx, new)
+        ref = C.reference(clean)
+        ref["lse"][rows] = np.nan                # checked above
+        B.check(C.to64(r["out"]), C.to64(r["lse"]), ref, dtype, dim)
