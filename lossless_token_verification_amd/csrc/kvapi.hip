@@ -105,12 +105,19 @@ size_t pad256(size_t n) { return (n + 255) / 256 * 256; }
 // max_new, or the batch's mean, times the heads of a group).  Smaller tiles read
 // the keys again, larger ones compute rows that are not there (head_dim 128, B =
 // 128 over 2300 positions: 36 rows 387 us in tiles of 32, 214 of 64, 237 of 128; 4
-// rows 195, 198, 225).  wgs: items to aim at where keys are split, one for each
-// workgroup the chip holds.  min_units: a split costs a row 8 bytes of partial
-// result per element, written and read, a position 4 of cache; 4 positions per
-// row and 64 at least measured best where splits are that short, on a chip that is
-// not full (9 rows x 4 heads over 4000 positions: 26 us with 16 positions per row,
-// 17 with 4).
+// rows 195, 198, 225).  wgs: items to aim at where keys are split, for most shapes
+// the workgroups that the chip holds by registers and LDS (2 to 4 a CU; float32 at
+// head_dim 128, 512 against 1024: single tokens over 2300 positions at B = 16 65
+// against 79 us, B = 64 220 against 237).  Matrix tiles of 32 rows up to head_dim
+// 128, and of 64 at head_dim 64, fit 4 to 8 times a CU; fewer and longer splits
+// than that measured better (single tokens, head_dim 128, 768 against 1024: B = 64
+// over 2300 positions 95 against 101 us, B = 4 over 110000 275 against 277; head_dim
+// 64, 1024 against 2048: B = 128 over 2300 96 against 102; 9 tokens there, 1024
+// against 1280: B = 16 over 4000 35 against 39).  min_units: a split costs a row 8
+// bytes of partial result per element, written and read, a position 4 of cache; 4
+// positions per row and 64 at least measured best where splits are that short, on a
+// chip that is not full (9 rows x 4 heads over 4000 positions: 26 us with 16
+// positions per row, 17 with 4).
 sv::AttendShape attend_shape(const spec_kv_attention_desc& d) {
   sv::AttendShape s{};
   const int D = d.head_dim;
@@ -127,7 +134,7 @@ sv::AttendShape attend_shape(const spec_kv_attention_desc& d) {
   } else {
     s.mt = D <= 64 ? sv::kRowsMT64 : D <= 128 ? sv::kRowsMT128 : sv::kRowsMT256;
     s.kt = sv::kRowsKT;
-    s.wgs = 1024;
+    s.wgs = D > 64 ? 512 : 1024;
     s.min_units = 256 / s.kt;
   }
   return s;

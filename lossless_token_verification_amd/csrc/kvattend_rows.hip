@@ -11,9 +11,9 @@
 // largest values add up without overflow.
 //
 // Single tokens are bound by the pages' bandwidth (B = 64 over 2300 positions, 32
-// query and 8 key heads of 128: 1.2 GB in 240 us, 5.0 TB/s), more rows by the
+// query and 8 key heads of 128: 1.2 GB in 220 us, 5.5 TB/s), more rows by the
 // vector units, which read a key once for 4 rows (2 above head_dim 128, for the
-// registers): 9 tokens over the same 1.19 ms, 18 TF.
+// registers): 9 tokens over the same 1.18 ms, 18 TF.
 #include "kvattend.h"
 
 namespace sv {

@@ -26,7 +26,7 @@ def sv():
     (60, 140, 256, 64, "bf16", 1),       # 5 tiles of 32 rows for 4 places a head
     (10, 200, 128, 128, "f16", 1),       # 7 for 6
     (70, 160, 64, 64, "f32", 0),         # 40 tiles of 4 rows for 16
-    (1, 40, 128, 248, "f32", 0),         # 20 of 2 for 8
+    (1, 40, 128, 248, "f32", 0),         # 20 of 2 for 4
     (9, 150, 256, 256, "bf16", 0)])      # 3 tiles of 64 rows for 2
 def test_one_sequence_of_more_tiles_than_places(sv, ctx, new, heads, dim, dtype, hint):
     """A single sequence whose tiles alone fill the chip, on a table so wide that its
