@@ -93,7 +93,6 @@ struct SlotInfo {
   int32_t split, splits;   // which split of its tile this slot holds, of how many
   int32_t token0, row0;    // the sequence's first token row, the tile's first query row
   int32_t rows;            // query rows of the tile
-  int32_t unused[3];
 };
 
 // Element types, as in the C ABI.
