@@ -122,7 +122,7 @@ typedef struct {
  *               v_stride elements apart (parts of a fused projection's rows)
  *   slot_map    [T] device int64
  * Rows and caches that lie on 16-byte boundaries are copied 16 bytes at a
- * time, others by the element (correct, slower). */
+ * time, others by the element (correct, at half the rate). */
 int32_t kv_cache_append(const spec_kv_append_desc* desc, const void* k, const void* v,
                         const int64_t* slot_map, void* k_cache, void* v_cache,
                         void* hip_stream);
@@ -138,8 +138,9 @@ typedef struct {
   int32_t max_blocks;     /* >= 0 columns of the block table                     */
   int32_t dtype;          /* SV_DTYPE_F32, _BF16 or _F16: q, caches and out alike */
   int32_t sliding_window; /* W > 0: a token sees itself and the W - 1 before it; 0: all */
-  int32_t max_new;        /* the most new tokens of any sequence, 0 if unknown: picks the
-                             tile shape, never the result's validity              */
+  int32_t max_new;        /* the most new tokens of any sequence, 0 if unknown (the batch's
+                             mean then): picks the tile shape, one for the call, and the
+                             workspace's size, never the result's validity        */
   int32_t reserved;       /* must be 0                                           */
   int64_t q_stride;       /* elements between q's token rows; 0 => heads * head_dim */
   int64_t block_stride;   /* elements between blocks of a cache; 0 =>

@@ -77,11 +77,13 @@ struct AttendPlanShared {
 // sum tiles * ceil(units / S) <= want_items follows from, or units /
 // (want_items / 2) where there is no such room.  There are never more than
 // want_items + tiles items, which bounds the launch; the sequences that are
-// split have units > S, so they use at most 2 want_items partial slots.  Items are numbered from the longest class of splits to the
-// shortest, so that the last workgroups to start are the short ones (B = 256,
-// 512 to 4096 positions: 474 -> 437 us).  Every workgroup makes these sums
-// itself (passes over the batch from cache), which costs less than the launch
-// that a separate planning kernel would be.
+// split have units > S, so they use at most 2 want_items partial slots.  Items are
+// numbered from the longest class of splits to the shortest, so that the last
+// workgroups to start are the short ones (B = 256, 512 to 4096 positions: 474 -> 437
+// us).  Every workgroup makes these sums itself, three or four passes over the batch
+// from cache, which costs less than the launch that a separate planning kernel
+// would be up to some 2000 sequences (single tokens over 1000 positions: 6.0 TB/s
+// of pages at 2048 of them, 5.2 at 4096).
 template <int MT, int KT, int WAVES>
 __device__ __forceinline__ bool attend_find(const AttendArgs& a, int x, bool count_slots,
                                             AttendPlanShared<WAVES>& sh, AttendItem& it) {

@@ -40,14 +40,15 @@
 //
 // What bounds it and what it measured (bf16, 32 query and 8 key heads of 128):
 // up to 64 rows the pages' bandwidth (B = 256 verifications of 9 tokens over 512
-// to 4096 positions: 2.60 GB in 422 to 427 us, 6.1 TB/s; B = 4 single tokens over 90000
-// to 131071: 2.08 GB in 319 to 327 us, 6.4 to 6.5 TB/s; a plain read of such an amount runs at
-// 6.9).  With 128 rows the matrix cores and the exponentials in turn, at the
-// clock that the power limit leaves (1.96 GHz): 4 prompts of 2048 to 4096 tokens
-// 332 GF in 385 to 407 us, 815 to 860 TF; 16384 tokens 1000 TF (head_dim 64: 870).
-// Other head sizes cost what the next of the three costs (B = 64, 9 tokens over
-// 2300 positions: 85 us at 80, 87 at 96, 172 at 192, against 1.09, 1.08 and 2.02 ms
-// on the vector units).
+// to 4096 positions: 2.60 GB in 426 to 428 us, 6.1 TB/s; B = 4 single tokens over 90000
+// to 131071: 2.08 GB in 321 to 324 us, 6.4 to 6.5 TB/s; a plain read of such an amount runs at
+// 6.9).  With 128 rows the matrix cores (busy 42 % of the cycles) and the vector
+// units (53 %), which a wavefront uses in turn and two to a SIMD do not overlap
+// further: 4 prompts of 2048 to 4096 tokens 332 GF in 377 to 397 us, 836 to 881 TF;
+// 16384 tokens 1000 TF (head_dim 64: 870).  Head sizes between the three move
+// fewer bytes in little less time, since buffers, steps and tiles are the next
+// one's (B = 64, 9 tokens over 2300 positions: 80 us at 80, 85 at 96, 98 at 128, 170
+// at 192, 220 at 256).
 #pragma once
 
 #include <type_traits>

@@ -15,9 +15,13 @@
 // kFusedTokens tokens, fills the token arrays itself; beyond that a second
 // launch spreads the fill over the chip.  A batch of one thread per sequence
 // keeps the sums' results in LDS for the fill and scans by lane moves on the
-// vector unit.  One sequence and token takes 2.9 us on the device, B = 256 with 9
-// tokens each 6.6, B = 64 prompts of up to 4096 (145000 rows) 4.3 and 8.2 for the
-// fill; a call spends 8 to 10 us on the host.
+// vector unit.  One sequence and token takes 2.8 us on the device, B = 256 with 9
+// tokens each 6.4, B = 64 prompts of up to 4096 (145000 rows) 4.3 and 7.9 for the
+// fill; a call spends 8 to 10 us on the host.  The fill is a launch of its own
+// because it reads what the first one wrote (sums, and freed blocks pushed); each
+// of its workgroups makes the sums of the taken blocks again.  More sequences than
+// threads go in chunks, three scans each: a call takes 20 us at 2048 single tokens,
+// 37 at 4096, 0.22 ms at 16384 and 0.85 ms at 65536.
 #include "kv_args.h"
 
 namespace sv {
