@@ -1,0 +1,505 @@
+"""Timed cases of the paged cache's rotated and 4-bit operators: writing keys with
+their position rotation (rope), writing them to a cache held in 4 bits and
+reading the rows back as they stand there (store), and the attention of new
+tokens over the 4-bit pages (attend).
+
+A case is a dict of plain values; lengths follow from the case alone, values and
+block orders from the seed.  ``own`` picks the side ``run`` takes: elementary
+torch operations (False) or the package's calls.
+
+The 4-bit cache: a code is a sign and one of the levels 0, 0.5, 1, 1.5, 2, 3, 4, 6
+(two codes a byte, the even channel in the low half).  Keys have a power of two
+per 32 channels, kept as its exponent + 127 (255: not a number): the least one
+with amax <= 7 of it.  Values have one scale a row, amax / 6 rounded to bfloat16
+and kept as float32.  A code is the level nearest to x / scale, ties to the even
+code.
+"""
+
+import math
+import random
+
+import torch
+
+own = False
+
+DEV = "cuda"
+DTYPES = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
+LEVELS = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
+
+
+def listed():
+    return [
+        # one request decoding alone: its query, key and value of a token
+        dict(name="rope_token_b1", op="rope", batch=1, ctx_lo=1000, ctx_hi=1000, new_lo=1, new_hi=1,
+             block=16, heads=32, kv_heads=8, dim=128, rot=128, pairs=False, dtype="bf16", pad=0),
+        # the verification step of 256 sequences: 8 drafts and the token before them each
+        dict(name="rope_verify_b256", op="rope", batch=256, ctx_lo=512, ctx_hi=4096, new_lo=9,
+             new_hi=9, block=16, heads=32, kv_heads=8, dim=128, rot=128, pairs=False, dtype="bf16",
+             pad=0),
+        # four long prompts
+        dict(name="rope_prompt_b4", op="rope", batch=4, ctx_lo=0, ctx_hi=0, new_lo=4000, new_hi=4096,
+             block=16, heads=32, kv_heads=8, dim=128, rot=128, pairs=False, dtype="bf16", pad=0),
+        # odd counts, a part of each head rotated in neighbouring pairs, a padded batch
+        dict(name="rope_odd_b37", op="rope", batch=37, ctx_lo=0, ctx_hi=777, new_lo=0, new_hi=33,
+             block=24, heads=15, kv_heads=5, dim=80, rot=48, pairs=True, dtype="f16", pad=100),
+        # the verification step into a 4-bit cache
+        dict(name="store_verify_b256", op="store", batch=256, ctx_lo=512, ctx_hi=4096, new_lo=9,
+             new_hi=9, block=16, heads=32, kv_heads=8, dim=128, rot=128, pairs=False, dtype="bf16",
+             pad=0),
+        # four long prompts into it
+        dict(name="store_prompt_b4", op="store", batch=4, ctx_lo=0, ctx_hi=0, new_lo=4000,
+             new_hi=4096, block=16, heads=32, kv_heads=8, dim=128, rot=128, pairs=False,
+             dtype="bf16", pad=0),
+        # odd counts and pages, no rotation on the way (the keys come rotated)
+        dict(name="store_odd_b37", op="store", batch=37, ctx_lo=0, ctx_hi=777, new_lo=0, new_hi=33,
+             block=24, heads=15, kv_heads=5, dim=96, rot=0, pairs=False, dtype="f16", pad=100),
+        # one request decoding alone over 4-bit pages
+        dict(name="attend_token_b1", op="attend", batch=1, ctx_lo=1000, ctx_hi=1000, new_lo=1,
+             new_hi=1, block=16, heads=32, kv_heads=8, dim=128, dtype="bf16", window=0, lse=False),
+        # the verification step over its contexts
+        dict(name="attend_verify_b256", op="attend", batch=256, ctx_lo=512, ctx_hi=4096, new_lo=9,
+             new_hi=9, block=16, heads=32, kv_heads=8, dim=128, dtype="bf16", window=0, lse=False),
+        # a few requests deep into long contexts, one token each
+        dict(name="attend_token_long_b4", op="attend", batch=4, ctx_lo=90000, ctx_hi=131071,
+             new_lo=1, new_hi=1, block=16, heads=32, kv_heads=8, dim=128, dtype="bf16", window=0,
+             lse=True),
+        # whole prompts, nothing cached before
+        dict(name="attend_prompt_b4", op="attend", batch=4, ctx_lo=0, ctx_hi=0, new_lo=2048,
+             new_hi=4096, block=16, heads=32, kv_heads=8, dim=128, dtype="bf16", window=0,
+             lse=False),
+        # prompts and single tokens in one batch, a sliding window, wide heads, odd pages
+        dict(name="attend_mixed_b48", op="attend", batch=48, ctx_lo=0, ctx_hi=2000, new_lo=1,
+             new_hi=200, block=24, heads=8, kv_heads=8, dim=256, dtype="f16", window=257, lse=True),
+    ]
+
+
+def _log(rng, lo, hi):
+    """An integer of [lo, hi], spread over its logarithm."""
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    """A case that costs no more than the largest listed ones."""
+    while True:
+        case = _draw(rng)
+        cost = work(case)
+        if cost["bytes"] < 3.9e8 and cost["flops"] < 3.3e11:
+            return case
+
+
+def _draw(rng):
+    op = rng.choice(["rope", "store", "attend", "attend"])
+    kind = rng.choice(["tokens", "verify", "prompts"])
+    if op == "attend" and kind != "prompts":
+        # decoding and verification: any batch, contexts up to the long ones
+        batch = _log(rng, 1, 256)
+        hi = _log(rng, 17, min(131072, 1000000 // batch))
+        new = 1 if kind == "tokens" else rng.randint(2, 16)
+        lo, new_lo, new_hi = rng.randint(0, hi), 1 if rng.random() < 0.5 else new, new
+    elif op == "attend":
+        batch = _log(rng, 1, 16)
+        new_hi = _log(rng, 17, 8192 // batch)
+        hi = _log(rng, 1, 4096)
+        lo, new_lo = rng.randint(0, hi), rng.randint(1, new_hi)
+    elif kind == "prompts":
+        batch = _log(rng, 1, 64)
+        new_hi = _log(rng, 17, 16384 // batch)
+        lo, hi, new_lo = 0, rng.randint(0, 100), rng.randint(0, new_hi)
+    else:
+        batch = _log(rng, 1, 256)
+        hi = _log(rng, 17, 4096)
+        new_hi = 1 if kind == "tokens" else rng.randint(2, 16)
+        lo, new_lo = rng.randint(0, hi), rng.randint(0, new_hi)
+    kv = rng.choice([1, 2, 3, 4, 5, 8])
+    group = rng.choice([1, 2, 3, 4, 7, 8])
+    case = dict(op=op, batch=batch, ctx_lo=lo, ctx_hi=hi, new_lo=new_lo, new_hi=new_hi,
+                block=rng.choice([8, 16, 16, 24, 32, 64, 5]), heads=kv * group, kv_heads=kv)
+    if op == "attend":
+        case.update(dim=rng.choice([32, 64, 96, 128, 128, 192, 256]),
+                    dtype=rng.choice(["bf16", "f16"]), lse=rng.random() < 0.5,
+                    window=rng.choice([0, 0, rng.randint(1, 2000)]))
+        return case
+    dim = rng.choice([40, 64, 80, 96, 128, 128, 256] if op == "rope" else
+                     [32, 64, 96, 128, 128, 160, 256])
+    rots = [dim, dim, dim // 2, 2 * rng.randint(1, dim // 2)]
+    case.update(dim=dim, rot=rng.choice(rots if op == "rope" else rots + [0]),
+                pairs=rng.random() < 0.4, dtype=rng.choice(["bf16", "f16", "f32"]),
+                pad=rng.choice([0, 13]))
+    return case
+
+
+def _lengths(case):
+    """The contexts and new tokens of a case's sequences."""
+    rng = random.Random("%(batch)d %(ctx_lo)d %(ctx_hi)d %(new_lo)d %(new_hi)d" % case)
+    ctx = [rng.randint(case["ctx_lo"], case["ctx_hi"]) for _ in range(case["batch"])]
+    new = [rng.randint(case["new_lo"], case["new_hi"]) for _ in range(case["batch"])]
+    new[0] = max(new[0], 1)
+    return ctx, new
+
+
+def _ceil(a, b):
+    return -(-a // b)
+
+
+def _ints(values, dtype=torch.int32):
+    return torch.tensor(values, dtype=dtype, device=DEV)
+
+
+def _cumulated(new):
+    return [sum(new[:b]) for b in range(len(new) + 1)]
+
+
+def _tables(lens, block, width, g):
+    """Block tables for these lengths, ids in random order; (table, blocks used)."""
+    need = [_ceil(n, block) for n in lens]
+    total = sum(need)
+    order = torch.randperm(max(total, 1), generator=g, device=DEV).to(torch.int32)
+    first = _ints(_cumulated(need)[:-1], torch.int64)
+    at = torch.arange(width, device=DEV)
+    has = at[None] < _ints(need)[:, None]
+    table = torch.where(has, order[(first[:, None] + at).clamp(max=max(total - 1, 0))], -1)
+    return table.to(torch.int32).contiguous(), total
+
+
+def _cos_sin(rows, rot):
+    """The rotation's table [rows, rot]: cosines, then sines; angles in 64 bits."""
+    inv = 10000.0 ** (-torch.arange(0, rot, 2, device=DEV, dtype=torch.float64) / rot)
+    angle = torch.arange(rows, device=DEV, dtype=torch.float64)[:, None] * inv
+    return torch.cat([angle.cos(), angle.sin()], 1).float()
+
+
+def _key_codes(x):
+    """Codes and scale bytes of key rows [..., dim] in float32."""
+    g = x.view(*x.shape[:-1], -1, 32)
+    top = g.abs().amax(-1)
+    part, power = torch.frexp(top)                  # top = part * 2^power, part in [0.5, 1)
+    byte = (torch.where(part > 0.875, power + 1, power) - 3 + 127).clamp(0, 254)
+    byte = torch.where(top > 0, byte, 0)
+    byte = torch.where(torch.isfinite(top), byte, 255)
+    unit = torch.ldexp(torch.ones((), dtype=torch.float64, device=x.device), byte - 127)
+    codes = _codes(g / unit[..., None].float().clamp(min=2.0 ** -126))
+    return codes.view(x.shape), byte.to(torch.uint8)
+
+
+def _value_codes(x):
+    """Codes and scales of value rows [..., dim] in float32."""
+    scale = (x.abs().amax(-1) / 6).bfloat16().float()
+    bad = ~torch.isfinite(scale)
+    level = x.double() / torch.where(scale > 0, scale, math.inf)[..., None]
+    return _codes(level), torch.where(bad, math.nan, scale)
+
+
+def _codes(level):
+    """The nearest level's code, ties to the even code; the sign in bit 3."""
+    a = level.abs()
+    code = (a > 0.25).to(torch.uint8)
+    code += a >= 0.75
+    code += a > 1.25
+    code += a >= 1.75
+    code += a > 2.5
+    code += a >= 3.5
+    code += a > 5.0
+    return code | (torch.signbit(level).to(torch.uint8) << 3)
+
+
+def _packed(codes):
+    return codes[..., 0::2] | (codes[..., 1::2] << 4)
+
+
+def _unpacked(packed):
+    """The levels of packed codes, in float32."""
+    level = torch.tensor(LEVELS + tuple(-v for v in LEVELS), device=packed.device)
+    both = torch.stack([level.repeat(16), level.repeat_interleave(16)], 1)   # of a byte
+    return both[packed.int()].flatten(-2)
+
+
+def _key_scales(packed, byte):
+    """The power of two of every channel."""
+    groups = packed.shape[-1] // 16
+    b = byte[..., :groups].int()
+    unit = torch.where(b == 255, math.nan, torch.ldexp(torch.ones((), device=b.device), b - 127))
+    return unit.repeat_interleave(32, -1)
+
+
+def _empty_cache(blocks, kv, block, dim):
+    z = dict(dtype=torch.uint8, device=DEV)
+    return dict(k_codes=torch.zeros((blocks, kv, block, dim // 2), **z),
+                k_scales=torch.zeros((blocks, kv, block, 4 * _ceil(dim, 128)), **z),
+                v_codes=torch.zeros((blocks, kv, block, dim // 2), **z),
+                v_scales=torch.zeros((blocks, kv, block), dtype=torch.float32, device=DEV))
+
+
+def prepare(case, seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    ctx, new = _lengths(case)
+    block, heads, kv, dim = case["block"], case["heads"], case["kv_heads"], case["dim"]
+    dt, op = DTYPES[case["dtype"]], case["op"]
+    lens = [c + n for c, n in zip(ctx, new)]
+    s = dict(op=op, block=block, tokens=sum(new), max_new=max(new), max_len=max(lens))
+    table, used = _tables(lens, block, _ceil(max(lens), block) + 1, g)
+    rows = s["tokens"] + case.get("pad", 0)
+    # q, k and v are the three parts of each row of one fused product
+    qkv = torch.randn((rows, (heads + 2 * kv) * dim), generator=g, device=DEV).to(dt)
+    s["q"] = qkv[:, :heads * dim].view(rows, heads, dim)
+    shape = (used + 1, kv, block, dim)
+    if op == "attend":
+        # keys whose channels differ in strength, as those of trained models do
+        cache = _empty_cache(*shape)
+        strength = torch.exp(0.5 * torch.randn((kv, 1, dim), generator=g, device=DEV))
+        x = (torch.randn(shape, generator=g, device=DEV) * strength).to(dt).float()
+        codes, byte = _key_codes(x)
+        cache["k_codes"], cache["k_scales"][..., :dim // 32] = _packed(codes), byte
+        codes, cache["v_scales"] = _value_codes(torch.randn(shape, generator=g, device=DEV).to(dt).float())
+        cache["v_codes"] = _packed(codes)
+        s.update(cache=cache, table=table, seq_lens=_ints(lens), cu_tokens=_ints(_cumulated(new)),
+                 window=case["window"], lse=case["lse"])
+        return s
+    seq = _ints([b for b, n in enumerate(new) for _ in range(n)], torch.int64)
+    pos = _ints([c + j for c, n in zip(ctx, new) for j in range(n)], torch.int64)
+    slots = torch.full((rows,), -1, dtype=torch.int64, device=DEV)
+    slots[:s["tokens"]] = table[seq, pos // block].to(torch.int64) * block + pos % block
+    positions = torch.full((rows,), -1, dtype=torch.int32, device=DEV)
+    positions[:s["tokens"]] = pos.to(torch.int32)
+    s.update(k=qkv[:, heads * dim:(heads + kv) * dim].view(rows, kv, dim),
+             v=qkv[:, (heads + kv) * dim:].view(rows, kv, dim), slot_map=slots,
+             positions=positions, pairs=case["pairs"], rot=case["rot"],
+             cos_sin=_cos_sin(s["max_len"], case["rot"]) if case["rot"] else None)
+    if op == "rope":
+        s.update(k_cache=torch.randn(shape, generator=g, device=DEV).to(dt),
+                 v_cache=torch.randn(shape, generator=g, device=DEV).to(dt))
+    else:
+        s["cache"] = _empty_cache(*shape)
+    s["out"] = torch.zeros((rows, heads, dim), dtype=dt, device=DEV)
+    return s
+
+
+def _turned(x, cos_sin, positions, pairs):
+    """Rows [T, heads, dim] turned by their positions' angles, as wide as the table."""
+    rot = cos_sin.shape[1]
+    at = cos_sin[positions][:, None].to(x.dtype)
+    cos, sin = at[..., :rot // 2], at[..., rot // 2:]
+    if pairs:
+        a, b = x[..., 0:rot:2], x[..., 1:rot:2]
+        turned = torch.stack([a * cos - b * sin, b * cos + a * sin], -1).flatten(-2)
+    else:
+        a, b = x[..., :rot // 2], x[..., rot // 2:rot]
+        turned = torch.cat([a * cos - b * sin, b * cos + a * sin], -1)
+    return torch.cat([turned, x[..., rot:]], -1)
+
+
+def _plain_rope(s):
+    rows = torch.nonzero(s["slot_map"] >= 0)[:, 0]
+    pos, at, block = s["positions"][rows], s["slot_map"][rows], s["block"]
+    dt = s["q"].dtype
+    s["out"][rows] = _turned(s["q"][rows].float(), s["cos_sin"], pos, s["pairs"]).to(dt)
+    k = _turned(s["k"][rows].float(), s["cos_sin"], pos, s["pairs"]).to(dt)
+    s["k_cache"][at // block, :, at % block] = k
+    s["v_cache"][at // block, :, at % block] = s["v"][rows]
+    return dict(q=s["out"], k_cache=s["k_cache"], v_cache=s["v_cache"])
+
+
+def _plain_store(s):
+    rows = torch.nonzero(s["slot_map"] >= 0)[:, 0]
+    at, block, dt, c = s["slot_map"][rows], s["block"], s["q"].dtype, s["cache"]
+    k = s["k"][rows].double()      # 64 bits: keys next to a border between two levels
+    if s["rot"]:
+        pos = s["positions"][rows]
+        s["out"][rows] = _turned(s["q"][rows].float(), s["cos_sin"], pos, s["pairs"]).to(dt)
+        k = _turned(k, s["cos_sin"], pos, s["pairs"])
+    page, row = at // block, at % block
+    codes, byte = _key_codes(k.float())
+    c["k_codes"][page, :, row] = _packed(codes)
+    c["k_scales"][page, :, row, :byte.shape[-1]] = byte
+    codes, scale = _value_codes(s["v"][rows].float())
+    c["v_codes"][page, :, row] = _packed(codes)
+    c["v_scales"][page, :, row] = scale
+    # the rows as they stand in the cache
+    k, v = torch.zeros_like(s["k"]), torch.zeros_like(s["v"])
+    packed = c["k_codes"][page, :, row]
+    k[rows] = (_unpacked(packed) * _key_scales(packed, c["k_scales"][page, :, row])).to(dt)
+    v[rows] = (_unpacked(c["v_codes"][page, :, row]) * c["v_scales"][page, :, row, None]).to(dt)
+    return dict(q=s["out"], k=k, v=v) if s["rot"] else dict(k=k, v=v)
+
+
+def _plain_attend(s):
+    q, table, block, c = s["q"], s["table"], s["block"], s["cache"]
+    lens, cu = s["seq_lens"].long(), s["cu_tokens"].long()
+    T, heads, dim = q.shape
+    kv = c["k_codes"].shape[1]
+    group, B, n_max = heads // kv, len(lens), s["max_new"]
+    n = cu[1:] - cu[:-1]
+    j = torch.arange(n_max, device=DEV)
+    row = (cu[:-1, None] + j).clamp(max=T - 1)
+    pos = (lens - n)[:, None] + j                                   # [B, n_max]
+    key = torch.arange(s["max_len"], device=DEV)
+    page, at = table[:, key // block].long().clamp(min=0), (key % block)[None]
+    held = (key[None] < lens[:, None])[:, :, None, None]
+    packed = c["k_codes"][page, :, at]                              # [B, keys, kv, dim / 2]
+    k = _unpacked(packed).mul_(_key_scales(packed, c["k_scales"][page, :, at]))
+    k = k.permute(0, 2, 3, 1).contiguous()
+    qp = q[row].float().view(B, n_max, kv, group, dim).permute(0, 2, 1, 3, 4)
+    score = torch.matmul(qp.reshape(B, kv, n_max * group, dim), k) * dim ** -0.5
+    del k, packed
+    v = _unpacked(c["v_codes"][page, :, at]).mul_(c["v_scales"][page, :, at, None])
+    v = v.masked_fill_(~held, 0.0).permute(0, 2, 1, 3).contiguous()
+    score = score.view(B, kv, n_max, group, -1)
+    seen = (key <= pos[:, :, None]) & (key < lens[:, None, None])
+    if s["window"]:
+        seen &= key > pos[:, :, None] - s["window"]
+    score.masked_fill_(~seen[:, None, :, None], -math.inf)
+    top = score.amax(-1, keepdim=True)
+    top = torch.where(top == -math.inf, 0.0, top)
+    p = score.sub_(top).exp_()
+    total = p.sum(-1, keepdim=True)
+    o = torch.matmul(p.view(B, kv, n_max * group, -1), v).view(B, kv, n_max, group, dim)
+    o = torch.where(total > 0, o / total, 0.0)
+    lse = (total.log() + top)[..., 0]
+    mine = j[None] < n[:, None]
+    out = dict(out=o.permute(0, 2, 1, 3, 4).reshape(B, n_max, heads, dim)[mine].to(q.dtype))
+    if s["lse"]:
+        out["lse"] = lse.permute(0, 2, 1, 3).reshape(B, n_max, heads)[mine]
+    return out
+
+
+def _own_run(s):
+    import lossless_token_verification_amd as sv
+    if s["op"] == "rope":
+        sv.kv_cache_append_rotary(s["q"], s["k"], s["v"], s["positions"], s["cos_sin"],
+                                  s["slot_map"], s["k_cache"], s["v_cache"],
+                                  interleaved=s["pairs"], out=s["out"])
+        return dict(q=s["out"], k_cache=s["k_cache"], v_cache=s["v_cache"])
+    if s["op"] == "store":
+        turn = dict(q=s["q"], positions=s["positions"], cos_sin=s["cos_sin"],
+                    interleaved=s["pairs"], out=s["out"]) if s["rot"] else {}
+        sv.kv_cache_append_q4(s["k"], s["v"], s["slot_map"], s["cache"], **turn)
+        k, v = sv.kv_cache_read_q4(s["slot_map"], s["cache"], s["k"].dtype)
+        return dict(q=s["out"], k=k, v=v) if s["rot"] else dict(k=k, v=v)
+    r = sv.kv_paged_attention_q4(s["q"], s["cache"], s["table"], s["seq_lens"], s["cu_tokens"],
+                                 sliding_window=s["window"], max_new=s["max_new"], lse=s["lse"])
+    return dict(out=r["out"], lse=r["lse"]) if s["lse"] else dict(out=r["out"])
+
+
+def run(state):
+    if own:
+        return _own_run(state)
+    return {"rope": _plain_rope, "store": _plain_store, "attend": _plain_attend}[state["op"]](state)
+
+
+def _keys(case):
+    """Keys read (once for each sequence) and (row, key) pairs of an attention case."""
+    w, pairs = case["window"], 0
+    both = list(zip(*_lengths(case)))
+    keys = sum((c + n) - (max(0, c + 1 - w) if w else 0) for c, n in both if n)
+    pairs = sum(min(p + 1, w) if w else p + 1 for c, n in both for p in range(c, c + n))
+    return keys, pairs
+
+
+def work(case):
+    ctx, new = _lengths(case)
+    T, B, dim, kv = sum(new), case["batch"], case["dim"], case["kv_heads"]
+    size = 4 if case["dtype"] == "f32" else 2
+    q, row = case["heads"] * dim * size, kv * dim * size          # of a token
+    held = kv * (dim + 4 * _ceil(dim, 128) + 4)                   # bytes of a position in 4 bits
+    if case["op"] == "attend":
+        keys, pairs = _keys(case)
+        return dict(bytes=keys * held + T * q * 2 + _ceil(keys, case["block"]) * 4 + B * 8 +
+                    (T * case["heads"] * 4 if case["lse"] else 0),
+                    flops=4 * dim * case["heads"] * pairs)
+    turn = T * 4 + min(T, max(c + n for c, n in zip(ctx, new))) * case["rot"] * 4 if case["rot"] else 0
+    if case["op"] == "rope":
+        return dict(bytes=T * (2 * q + 4 * row + 8) + turn, flops=T * (case["heads"] + kv) * case["rot"] * 3)
+    # rows in, codes out; codes in, rows out
+    return dict(bytes=T * ((2 * q if case["rot"] else 0) + 4 * row + 2 * held + 16) + turn,
+                flops=T * kv * dim * 4)
+
+
+def _exact_turn(x, s):
+    """Rows in 64 bits, turned as complex numbers."""
+    x, rot = x.double(), s["rot"]
+    if not rot:
+        return x
+    at = s["cos_sin"][s["positions"].clamp(min=0).long()].double()[:, None]
+    unit = torch.complex(at[..., :rot // 2], at[..., rot // 2:])
+    part = x[..., :rot].reshape(*x.shape[:-1], rot // 2, 2) if s["pairs"] else \
+        torch.stack([x[..., :rot // 2], x[..., rot // 2:rot]], -1)
+    z = torch.view_as_real(torch.view_as_complex(part.contiguous()) * unit)
+    z = z.flatten(-2) if s["pairs"] else torch.cat([z[..., 0], z[..., 1]], -1)
+    return torch.cat([z, x[..., rot:]], -1)
+
+
+def _exact_level(x):
+    """The level nearest to each number, ties to the even code."""
+    level = torch.tensor(LEVELS, dtype=torch.float64, device=DEV)
+    hi = torch.searchsorted(level, x.abs().contiguous()).clamp(max=7)
+    lo = (hi - 1).clamp(min=0)
+    down, up = x.abs() - level[lo], level[hi] - x.abs()
+    near = torch.where((down < up) | ((down == up) & (lo % 2 == 0)), lo, hi)
+    return level[near] * x.sign()
+
+
+def _placed(cache, rows, slots):
+    """The cache in 64 bits with each row at its slot, seen as one list of slots."""
+    pages, kv, block, dim = cache.shape
+    flat = cache.double().transpose(1, 2).reshape(pages * block, kv, dim)
+    flat = torch.cat([flat, flat[:1]])           # a place of its own for rows without one
+    flat[torch.where(slots < 0, pages * block, slots)] = rows.double()
+    return flat[:-1].view(pages, block, kv, dim).transpose(1, 2)
+
+
+def exact(case, seed):
+    """The operators by their definitions in 64 bits; attention a sequence and a key
+    head at a time."""
+    s = prepare(case, seed)
+    if case["op"] != "attend":
+        mine = (s["slot_map"] >= 0)[:, None, None]
+        q, k = torch.where(mine, _exact_turn(s["q"], s), 0.0), _exact_turn(s["k"], s)
+        if case["op"] == "rope":
+            return dict(q=q, k_cache=_placed(s["k_cache"], k, s["slot_map"]),
+                        v_cache=_placed(s["v_cache"], s["v"], s["slot_map"]))
+        groups = k.view(*k.shape[:2], -1, 32)
+        top = groups.abs().amax(-1, keepdim=True)
+        unit = torch.exp2(torch.ceil(torch.log2(top / 7)).clamp(-127, 127))
+        unit = torch.where(top > 7 * unit, unit * 2, torch.where(top <= 3.5 * unit, unit / 2, unit))
+        k = torch.where(mine, (_exact_level(groups / unit) * unit).view(k.shape), 0.0)
+        v = s["v"].double()
+        unit = (s["v"].float().abs().amax(-1, keepdim=True) / 6).bfloat16().double()
+        v = torch.where(mine, _exact_level(v / unit) * unit, 0.0)
+        return dict(q=q, k=k, v=v) if s["rot"] else dict(k=k, v=v)
+    ctx, new = _lengths(case)
+    T, heads, dim = s["q"].shape
+    kv, c = case["kv_heads"], s["cache"]
+    per = heads // kv
+    level = torch.tensor(LEVELS, dtype=torch.float64, device=DEV)
+    level = torch.cat([level, -level])
+
+    def values(codes):
+        return level[torch.stack([codes & 15, codes >> 4], -1).flatten(-2).int()]
+
+    out = torch.zeros((T, heads, dim), dtype=torch.float64, device=DEV)
+    lse = torch.full((T, heads), -math.inf, dtype=torch.float64, device=DEV)
+    at = 0
+    for b in range(case["batch"]):
+        L = ctx[b] + new[b]
+        pages = s["table"][b, :_ceil(L, case["block"])].long()
+        where = torch.arange(L, device=DEV)
+        for h in range(kv):
+            power = c["k_scales"][pages, h].reshape(-1, c["k_scales"].shape[-1])[:L, :dim // 32]
+            k = values(c["k_codes"][pages, h].reshape(-1, dim // 2)[:L])
+            k = k * torch.exp2(power.double() - 127).repeat_interleave(32, -1)
+            v = values(c["v_codes"][pages, h].reshape(-1, dim // 2)[:L])
+            v = v * c["v_scales"][pages, h].reshape(-1, 1)[:L].double()
+            for r0 in range(0, new[b], 2048):
+                r1 = min(new[b], r0 + 2048)
+                p = torch.arange(ctx[b] + r0, ctx[b] + r1, device=DEV)[:, None]
+                hidden = where > p
+                if case["window"]:
+                    hidden |= where <= p - case["window"]
+                for e in range(h * per, (h + 1) * per):
+                    x = s["q"][at + r0:at + r1, e].double() @ k.T / math.sqrt(dim)
+                    x[hidden] = -math.inf
+                    z = torch.logsumexp(x, 1)
+                    out[at + r0:at + r1, e] = torch.exp(x - z[:, None]) @ v
+                    lse[at + r0:at + r1, e] = z
+        at += new[b]
+    return dict(out=out, lse=lse) if case["lse"] else dict(out=out)
