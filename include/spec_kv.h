@@ -15,7 +15,11 @@
  *   kv_cache_append        writes the tokens' keys and values to their slots;
  *   kv_paged_attention     softmax attention of the new tokens over the pages:
  *                          one token, a drafted window, a chunk of a prompt or
- *                          a whole prompt per sequence, in one batch.
+ *                          a whole prompt per sequence, in one batch;
+ *   kv_cache_append_rotary the append with the position rotation of queries and
+ *                          keys on the way;
+ *   kv_cache_append_q4, kv_cache_read_q4, kv_paged_attention_q4
+ *                          the same with a cache held in 4 bits.
  *
  * Conventions (ownership, asynchrony, status codes, spec_verify_last_error,
  * thread safety) are spec_verify.h's; status codes and the F32 and BF16
@@ -189,6 +193,110 @@ int32_t kv_paged_attention(const spec_kv_attention_desc* desc, const void* q,
                            const int32_t* block_table, const int32_t* seq_lens,
                            const int32_t* cu_tokens, void* out, float* lse, void* workspace,
                            size_t workspace_bytes, void* hip_stream);
+
+/* ------------------------------------------------------------------------- */
+/* Rotated rows.                                                              */
+
+typedef struct {
+  int32_t tokens;         /* T >= 0 rows                                         */
+  int32_t heads;          /* query heads; 0: no queries                          */
+  int32_t kv_heads;       /* >= 1                                                */
+  int32_t head_dim;       /* >= 1; of a 4-bit cache a multiple of 32 up to
+                             SV_MAX_HEAD_DIM                                      */
+  int32_t block_size;     /* >= 1                                                */
+  int32_t num_blocks;     /* >= 0; num_blocks * block_size < 2^31                */
+  int32_t dtype;          /* SV_DTYPE_F32, _BF16 or _F16: rows (and 16 / 32-bit
+                             caches)                                             */
+  int32_t rotary_dim;     /* R: channels 0 .. R-1 of a head turn; even, up to
+                             head_dim (0, and heads 0: no rotation, 4-bit append
+                             only)                                               */
+  int32_t interleaved;    /* 0: channel i turns with i + R/2; 1: 2i with 2i + 1   */
+  int32_t table_rows;     /* rows of cos_sin: positions 0 .. table_rows - 1       */
+  int64_t q_stride;       /* elements between token rows; 0 => heads * head_dim   */
+  int64_t k_stride;       /*   (kv_heads * head_dim)                              */
+  int64_t v_stride;
+  int64_t q_out_stride;
+  int64_t block_stride;   /* elements between blocks of a cache; 0 => dense (as
+                             a 4-bit cache has to be)                            */
+} spec_kv_rotary_desc;
+
+/* kv_cache_append with the position rotation on the way: for a pair (x, y) of
+ * channels and its angle at the token's position,
+ *     x' = x cos - y sin,  y' = y cos + x sin,
+ * queries to q_out, keys to their slots; values and the channels behind R as they
+ * are.  Computed in float32, rounded once to the type.
+ *   q           [T, heads, head_dim] device (NULL if heads is 0), read-only
+ *   k, v        [T, kv_heads, head_dim] device, read-only
+ *   positions   [T] device int32 (kv_blocktable_extend's)
+ *   cos_sin     [table_rows, R] device float32: R/2 cosines, then R/2 sines of a
+ *               position's angles
+ *   slot_map    [T] device int64, as for kv_cache_append
+ *   q_out       [T, heads, head_dim] device; may be q itself (same stride), and
+ *               must not overlap it otherwise
+ * A row whose position is not in the table is skipped: neither its query nor its
+ * key and value are written.  A row without a slot is written to q_out alone.
+ * Whole 16-byte vectors that turn together (R a multiple of 16 bytes, of twice
+ * that unless interleaved) on 16-byte boundaries are the fast case, others go by
+ * the element. */
+int32_t kv_cache_append_rotary(const spec_kv_rotary_desc* desc, const void* q, const void* k,
+                               const void* v, const int32_t* positions, const float* cos_sin,
+                               const int64_t* slot_map, void* q_out, void* k_cache,
+                               void* v_cache, void* hip_stream);
+
+/* ------------------------------------------------------------------------- */
+/* A cache held in 4 bits.
+ *
+ * Four dense arrays, rows numbered as in the other caches ([num_blocks, kv_heads,
+ * block_size] rows of head_dim channels; about 0.27 of a 16-bit cache's bytes):
+ *   k_codes, v_codes  [.., head_dim / 2] bytes, channel 2i in the low half of byte
+ *                     i, 2i + 1 in the high half.  A code is a sign (bit 3) and a
+ *                     level: 0, 0.5, 1, 1.5, 2, 3, 4, 6 (e2m1);
+ *   k_scales          [.., 4 ceil(head_dim / 128)] bytes: byte g is b for channels
+ *                     32 g .. 32 g + 31, whose unit is 2^(b - 127); 255: not a
+ *                     number.  Bytes behind head_dim / 32 are not used;
+ *   v_scales          [..] float32: the unit of a whole row, not negative.
+ * The append picks the least 2^e with amax <= 7 * 2^e for the channels of a key
+ * (no less than 2^-127), amax / 6 rounded to 8 significant bits (float32, then to
+ * bfloat16's precision) for a value row, and for each channel the level nearest to
+ * x / unit, ties to the even code, 6 for what is larger.  A key's channels with an
+ * infinity or NaN among them are all NaN, and so is a value row with one. */
+
+/* kv_cache_append_rotary into a 4-bit cache (rotary_dim 0: the rows as they are;
+ * positions and cos_sin are not read then).  Keys are turned in float64 and
+ * rounded to float32 before they are coded.
+ *   k_codes, v_codes  16-byte aligned; k_scales, v_scales 4-byte aligned */
+int32_t kv_cache_append_q4(const spec_kv_rotary_desc* desc, const void* q, const void* k,
+                           const void* v, const int32_t* positions, const float* cos_sin,
+                           const int64_t* slot_map, void* q_out, void* k_codes, void* k_scales,
+                           void* v_codes, float* v_scales, void* hip_stream);
+
+/* The rows of the given slots as they stand in the cache, k and v [tokens,
+ * kv_heads, head_dim] dense and 16-byte aligned, rounded to dtype; rows of slots
+ * that are negative or past the cache are 0. */
+int32_t kv_cache_read_q4(int32_t tokens, int32_t kv_heads, int32_t head_dim,
+                         int32_t block_size, int32_t num_blocks, int32_t dtype,
+                         const int64_t* slot_map, const void* k_codes, const void* k_scales,
+                         const void* v_codes, const float* v_scales, void* k, void* v,
+                         void* hip_stream);
+
+/* Workspace bytes of kv_paged_attention_q4; as kv_paged_attention_workspace_bytes. */
+size_t kv_paged_attention_q4_workspace_bytes(const spec_kv_attention_desc* desc);
+
+/* kv_paged_attention over a 4-bit cache: q and out bfloat16 or float16 (desc.dtype),
+ * head_dim a multiple of 32, desc.block_stride 0, everything else as there.
+ * Products on the matrix cores, on the codes as they lie: a query is split into
+ * pieces of 4 significant bits, relative to the largest of 32 channels, whose sum is off
+ * by 2^-14 of that at most (bf16; 2^-19 in f16), a softmax weight times its
+ * value's scale into pieces relative to the largest of 32 positions, off by 2^-9 of
+ * that at most (bf16; 2^-14 in f16).  Sums are float32.  A query row with an
+ * infinity or NaN gets NaN in out and lse if it sees a position.  Values at
+ * positions a row does not see never reach it, whatever their scales hold. */
+int32_t kv_paged_attention_q4(const spec_kv_attention_desc* desc, const void* q,
+                              const void* k_codes, const void* k_scales, const void* v_codes,
+                              const float* v_scales, const int32_t* block_table,
+                              const int32_t* seq_lens, const int32_t* cu_tokens, void* out,
+                              float* lse, void* workspace, size_t workspace_bytes,
+                              void* hip_stream);
 
 #ifdef __cplusplus
 }

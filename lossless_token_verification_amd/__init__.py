@@ -19,6 +19,9 @@ Functions mirror the C entry points:
 * ``kv_blocktable_extend``, ``kv_cache_append``, ``kv_paged_attention`` -- the
   paged cache before a verification: blocks and slots for the new tokens, their
   keys and values, their attention (``include/spec_kv.h``, ``kv.py``);
+* ``kv_cache_append_rotary`` -- the append with the position rotation on the way;
+* ``make_kv_cache_q4``, ``kv_cache_append_q4``, ``kv_cache_read_q4``,
+  ``kv_paged_attention_q4`` -- the same cache held in 4 bits;
 * ``workspace_bytes``, ``validate``, ``device_status``, ``abi_version``.
 """
 
@@ -29,7 +32,9 @@ import torch
 
 from . import kv as _kv
 from .kv import (KV_EXPORTED, MAX_HEAD_DIM, SV_DTYPE_F16, kv_blocktable_extend,  # noqa: F401
-                 kv_cache_append, kv_paged_attention, kv_paged_attention_workspace_bytes)
+                 kv_cache_append, kv_cache_append_q4, kv_cache_append_rotary, kv_cache_read_q4,
+                 kv_paged_attention, kv_paged_attention_q4, kv_paged_attention_q4_workspace_bytes,
+                 kv_paged_attention_workspace_bytes, make_kv_cache_q4)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # SPEC_VERIFY_LIB names another build of the same library (the host-sanitizer

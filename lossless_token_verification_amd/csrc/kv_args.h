@@ -59,6 +59,57 @@ struct AppendArgs {
 };
 hipError_t launch_append(const AppendArgs& a, hipStream_t st);
 
+// Rows rotated by their positions on the way: the queries to q_out, keys (and
+// values as they are) to their slots, or, for the 4-bit append, the queries alone.
+struct RotaryArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  const int32_t* positions;
+  const float* cos_sin;      // [table_rows, rot]: cosines, then sines
+  const int64_t* slots;
+  void* q_out;
+  void* dst[2];              // k_cache, v_cache
+  int32_t T, heads, kv_heads, dim, rot, pairs, table_rows, block_size, num_slots;
+  int64_t q_stride, k_stride, v_stride, q_out_stride, block_stride;   // elements
+  // what one thread takes is a unit: a vector of a row, or, of a rotated half, the
+  // two vectors that turn into each other
+  int32_t turn_units, row_units, v_units;   // of a head: turned, all; of a value head
+  int32_t token_units;                      // T * token_units < 2^31
+  FastDiv bs, token, row, vrow;             // by block_size and the unit counts
+};
+hipError_t launch_rotary(const RotaryArgs& a, int dtype, bool wide, hipStream_t st);
+
+// Rows to and from the cache held in 4 bits.
+struct Q4RowsArgs {
+  const void* k;             // append: rows in
+  const void* v;
+  void* k_out;               // read: rows out
+  void* v_out;
+  const int32_t* positions;  // append; NULL without a rotation
+  const float* cos_sin;
+  const int64_t* slots;
+  uint8_t* k_codes;
+  uint8_t* k_scales;
+  uint8_t* v_codes;
+  float* v_scales;
+  int32_t T, kv_heads, dim, rot, pairs, table_rows, block_size, num_slots;
+  int32_t row_lanes;         // lanes of a row: a power of two, dim / 8 of them at work
+  int64_t k_stride, v_stride;
+  FastDiv bs, heads;         // by block_size, kv_heads
+};
+hipError_t launch_q4_append(const Q4RowsArgs& a, const RotaryArgs& q, int dtype, bool wide,
+                            bool q_wide, hipStream_t st);
+hipError_t launch_q4_read(const Q4RowsArgs& a, int dtype, hipStream_t st);
+
+// The caches of the attention over 4-bit pages.
+struct Q4Cache {
+  const uint8_t* k_codes;
+  const uint8_t* k_scales;
+  const uint8_t* v_codes;
+  const float* v_scales;
+};
+
 // Paged attention.  The query rows of a sequence, token-major with the heads
 // that share a key head next to each other (row r: token r / group, head
 // h * group + r % group), are cut into tiles of MT rows; the keys of a tile

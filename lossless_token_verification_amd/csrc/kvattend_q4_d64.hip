@@ -1,0 +1,11 @@
+// Attention over 4-bit pages for head sizes up to 64.
+#include "kvattend_q4_mx.h"
+
+namespace sv {
+
+hipError_t launch_attend_q4_d64(const AttendArgs& a, const Q4Cache& c, int dtype, int mt,
+                               hipStream_t st) {
+  return launch_q4_width<64>(a, c, dtype, mt, st);
+}
+
+}  // namespace sv

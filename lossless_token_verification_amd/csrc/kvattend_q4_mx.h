@@ -1,0 +1,492 @@
+// Paged attention over a cache held in 4 bits, on the matrix instructions that take
+// 4-bit operands with a power of two per 32 of their terms (head_dim 64, 128, 256,
+// and every other multiple of 32 in the next of these, the rest of a row zero).
+//
+// The codes are never unpacked.  Both products are formed transposed, as in the
+// 16-bit kernel (a lane holds one query row throughout):
+//     S^T = K Q^T     A = key codes from LDS with their block scales
+//     O^T += V^T P^T  A = value codes from LDS, transposed by the read
+// and what stands against the codes is split into pieces that the instructions take
+// at the 4-bit rate: 6-bit numbers (e2m3: 4 significant bits, magnitudes to 7.5)
+// with a power of two per 32.  A piece scaled so that the largest of its 32 is in
+// [2, 4) is off by at most an eighth, the next piece holds that remainder scaled by
+// 32: n pieces are off by 2^-(5n - 1) of the largest at most.
+//   Queries: 3 pieces for bfloat16 (2^-14 of the largest of 32 channels; its 8
+//   bits are held whole down to a 64th of that), 4 for float16 (2^-19).
+//   Weights times their value's scale: 2 pieces for bfloat16 (2^-9 of the largest
+//   of the 32 positions that a lane holds, half a step of that type at its largest),
+//   3 for float16 (2^-14).  The largest is taken anew for every 32 positions, so
+//   that many small weights far from a large one are not lost; the sum of the
+//   weights is taken before, in float32.
+// The products are exact in the instruction, their sums float32.  Codes hold no
+// infinity: a position that a row does not see has weight 0 and value scale 0, and
+// needs no more care than that.
+#pragma once
+
+#include "kvattend_mfma.h"
+#include "kvattend_q4.h"
+
+namespace sv {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x6 __attribute__((ext_vector_type(6)));
+typedef float f32x32 __attribute__((ext_vector_type(32)));
+
+// Codes (4 bits, A) times pieces (6 bits, B), each with its scale's byte.
+__device__ __forceinline__ f32x4 mma_q4(u32x4 codes, int code_scale, u32x6 piece, int piece_scale,
+                                        f32x4 c) {
+  const i32x8 x = {static_cast<int>(codes[0]), static_cast<int>(codes[1]),
+                   static_cast<int>(codes[2]), static_cast<int>(codes[3]), 0, 0, 0, 0};
+  const i32x8 y = {static_cast<int>(piece[0]), static_cast<int>(piece[1]),
+                   static_cast<int>(piece[2]), static_cast<int>(piece[3]),
+                   static_cast<int>(piece[4]), static_cast<int>(piece[5]), 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 2, 0, code_scale, 0,
+                                                          piece_scale);
+}
+
+// The N pieces of 32 numbers, even ones in x0 and odd ones in x1, the largest of
+// magnitude `top` (as bits).  The conversions read their sources while they write, so
+// their sources have to outlive them: the empty statements keep the registers apart.
+// Numbers below 2^-104 lose bits (the last piece's scale is 2^-118 at least).
+template <int N>
+__device__ __forceinline__ void split_pieces(f32x16 x0, f32x16 x1, uint32_t top, u32x6 (&piece)[N],
+                                             int (&scale)[N]) {
+  const int b = max(static_cast<int>(top >> 23), 25) - 1;
+#pragma unroll
+  for (int p = 0; p < N; ++p) {
+    const float s = __uint_as_float(static_cast<uint32_t>(min(b, 254) - 5 * p) << 23);
+    piece[p] = __builtin_amdgcn_cvt_scalef32_2xpk16_fp6_f32(x0, x1, s);
+    asm volatile("" : "+v"(piece[p]) : "v"(x0), "v"(x1), "v"(s));
+    scale[p] = b >= 254 ? 255 : b - 5 * p;     // infinity or NaN among them: NaN
+    if (p + 1 < N) {
+      f32x32 y = __builtin_amdgcn_cvt_scalef32_pk32_f32_fp6(piece[p], s);
+      asm volatile("" : "+v"(y) : "v"(piece[p]), "v"(s));
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        x0[i] -= y[2 * i];
+        x1[i] -= y[2 * i + 1];
+      }
+    }
+  }
+}
+
+template <typename T_, int D_, bool kPad_, int W_>
+struct Q4Cfg {
+  using T = T_;
+  static constexpr bool kPad = kPad_;
+  static constexpr int D = D_, W = W_, KT = kQ4KT, MT = 16 * W;
+  static constexpr bool kBf = std::is_same<T, __bf16>::value;
+  // pieces; at D = 64 two of a query's lie side by side in one step
+  static constexpr int PQ = D == 64 || !kBf ? 4 : 3, PP = kBf ? 2 : 3;
+  static constexpr int HALVES = D == 256 ? 2 : 1;          // steps along a row
+  static constexpr int QS = D == 64 ? PQ / 2 : PQ;         // steps of a half
+  static constexpr int ROW = D / 2;                        // bytes of a row of codes
+  static constexpr int NV = D / 32;                        // its 16-byte vectors
+  static constexpr int RPL = kWave / NV;                   // rows of one direct load
+  static constexpr int LOADS = KT / RPL;                   // of K and of V, per unit
+  static constexpr int SW = D == 256 ? 2 : 1;              // words of key scales a row
+  static constexpr int kV = KT * ROW, kKS = 2 * kV;        // bytes: V codes, key scales,
+  static constexpr int kVS = kKS + SW * KT * 4;            //   value scales
+  static constexpr int BYTES = kVS + KT * 4;
+  static constexpr int SUPER = 2 * KT, IDS = SUPER / kWave;
+  static constexpr int OT = D / 16;                        // result tiles
+  static constexpr bool kOnce = MT <= 64;                  // as in the 16-bit kernel
+};
+
+// LDS vector permutation of row r: vector v lies at v ^ swz(r), so that the 16 rows
+// that 16 lanes read transposed (4 neighbours in each of 4 places, 16 vectors in all)
+// fall on different banks.
+template <int D>
+__device__ __forceinline__ int swz_q4(int r) {
+  return D == 64 ? (r >> 3) & 1 : D == 128 ? (r >> 2) & 3 : (r >> 1) & 7;
+}
+
+template <class C>
+__global__ __launch_bounds__((C::W > 4 ? C::W : 4) * kWave) __attribute__((amdgpu_waves_per_eu(C::D == 256 && C::W <= 4 ? 1 : 2))) void
+attend_q4_kernel(AttendArgs a, Q4Cache cache) {
+  using T = typename C::T;
+  constexpr int D = C::D, KT = C::KT, ROW = C::ROW, NV = C::NV, RPL = C::RPL, OT = C::OT;
+  constexpr int IDS = C::IDS, HALVES = C::HALVES, QS = C::QS, PQ = C::PQ, PP = C::PP;
+  // (two LDS objects: a direct load into one is known to leave the other alone)
+  __shared__ __attribute__((aligned(1024))) char sb0[C::BYTES], sb1[C::BYTES];
+  __shared__ __attribute__((aligned(256))) int32_t sid[C::W * C::SUPER];
+  __shared__ AttendPlanShared<C::W> plan;
+  const int tid = threadIdx.x, lane = tid & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int dim = C::kPad ? a.D : D, row_bytes = dim / 2;
+  const int x = blockIdx.x / a.kv_heads, h = blockIdx.x - x * a.kv_heads;
+  AttendItem it;
+  if (!attend_find<C::MT, KT, C::W>(a, x, a.max_slots > 0 && blockIdx.x == 0, plan, it)) return;
+  if (it.splits > 1 && h == 0 && tid == 0) attend_slot_info(a, it);
+
+  // this lane's query row (rows past the tile repeat its last one) and the quarter
+  // of a step's 128 terms it holds
+  const int g = lane >> 4;
+  const int row = wave * 16 + (lane & 15);
+  int see_lo;
+  uint32_t see_span;     // the positions it sees: see_span of them from see_lo on, and that one
+  u32x6 qf[HALVES][QS];
+  int qs[HALVES][QS];
+  {
+    int token, head;
+    attend_row(a, it.token0, it.row0 + min(row, it.rows - 1), h, token, head);
+    const int pos = it.pos0 + token - it.token0;
+    const int key_last = min(pos, it.key_hi - 1);
+    const int key_first = a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
+    see_lo = key_last >= key_first ? key_first : INT32_MAX;
+    see_span = key_last >= key_first ? key_last - key_first : 0;
+    const T* qr = static_cast<const T*>(a.q) + token * a.q_stride + static_cast<int64_t>(head) * dim;
+#pragma unroll
+    for (int hf = 0; hf < HALVES; ++hf) {
+      const int group = D == 64 ? g & 1 : hf * 4 + g;      // its 32 channels
+      f32x16 x0, x1;
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        u32x4 w = {0, 0, 0, 0};
+        if (!C::kPad || group * 32 < dim) w = reinterpret_cast<const u32x4*>(qr)[group * 4 + i];
+        typedef T t8 __attribute__((ext_vector_type(8)));
+        const t8 v = __builtin_bit_cast(t8, w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          x0[i * 4 + j] = static_cast<float>(v[2 * j]);
+          x1[i * 4 + j] = static_cast<float>(v[2 * j + 1]);
+          top = max(top, __float_as_uint(x0[i * 4 + j]) & 0x7fffffffu);
+          top = max(top, __float_as_uint(x1[i * 4 + j]) & 0x7fffffffu);
+        }
+      }
+      u32x6 piece[PQ];
+      int scale[PQ];
+      split_pieces<PQ>(x0, x1, top, piece, scale);
+#pragma unroll
+      for (int s = 0; s < QS; ++s) {
+        qf[hf][s] = piece[D == 64 ? 2 * s : s];
+        qs[hf][s] = scale[D == 64 ? 2 * s : s];
+        if (D == 64 && g >= 2) {
+          qf[hf][s] = piece[D == 64 ? 2 * s + 1 : s];
+          qs[hf][s] = scale[D == 64 ? 2 * s + 1 : s];
+        }
+      }
+    }
+  }
+  // positions every row of the tile may see: units inside need no mask
+  const int all_hi = min(it.pos0 + fast_div(it.row0, a.grp), it.key_hi - 1);
+  const int pos_last = it.pos0 + fast_div(it.row0 + it.rows - 1, a.grp);
+  const int all_lo = a.window > 0 && pos_last >= a.window ? pos_last - a.window + 1 : 0;
+
+  const int32_t* table = a.table + static_cast<int64_t>(it.b) * a.max_blocks;
+  const int64_t head_rows = static_cast<int64_t>(h) * a.block_size;
+  const int64_t block_rows = static_cast<int64_t>(a.kv_heads) * a.block_size;
+  // Lane l looks up position base + l: its row number in the cache, and whether there
+  // is such a page.  Positions outside the item's range read the nearest one inside
+  // (and are masked); a missing page reads block 0.
+  auto nearest = [&](int base) { return min(max(base + lane, it.key_lo), it.key_hi - 1); };
+  auto entry = [&](int base) { return table + fast_div(nearest(base), a.bs); };
+  auto row_of = [&](int base, int id) -> int64_t {
+    const int key = nearest(base);
+    const int r = key - fast_div(key, a.bs) * a.block_size;
+    const int safe = id >= 0 && id < a.num_blocks ? id : 0;
+    return safe * block_rows + head_rows + r;
+  };
+  auto paged = [&](int id) -> uint64_t { return __ballot(id >= 0 && id < a.num_blocks); };
+
+  // Loads the unit at position `base` into LDS; r0, r1: row numbers of its halves of
+  // 64 positions.  Inside the item's range, with whole pages of rows, a load's address
+  // is one lane's row plus a lane constant and moves through scalar registers.
+  const int lq = lane / NV, lslot = lane & (NV - 1);
+  const bool whole_rows = a.block_size % RPL == 0;
+  auto load_unit = [&](int base, int64_t r0, int64_t r1, char* sb) {
+    const bool inside = whole_rows && base >= it.key_lo && base + KT <= it.key_hi;
+#pragma unroll
+    for (int i = 0; i < (C::LOADS + C::W - 1) / C::W; ++i) {
+      const int j = wave + i * C::W;                 // which RPL rows
+      if (C::LOADS % C::W != 0 && j >= C::LOADS) break;
+      const int from = j * RPL & (kWave - 1);
+      const bool upper = j * RPL >= kWave;
+      const int64_t mine = upper ? r1 : r0;
+      const int vec = lslot ^ swz_q4<D>(j * RPL + lq);
+      if (inside) {
+        const int lo = static_cast<int>(mine), hi = static_cast<int>(mine >> 32);
+        const uint32_t s0 = __builtin_amdgcn_readlane(lo, from);
+        const uint32_t s1 = __builtin_amdgcn_readlane(hi, from);
+        const int64_t r = static_cast<int64_t>((static_cast<uint64_t>(s1) << 32) | s0);
+        const uint32_t in = lq * row_bytes + vec * 16;
+        if (!C::kPad || vec * 16 < row_bytes) {
+          load_lds<C::kOnce>(cache.k_codes + r * row_bytes + in, sb + j * 1024);
+          load_lds<C::kOnce>(cache.v_codes + r * row_bytes + in, sb + C::kV + j * 1024);
+        }
+      } else {
+        const int64_t r = __shfl(static_cast<long long>(mine), from + lq, kWave);
+        if (!C::kPad || vec * 16 < row_bytes) {
+          load_lds<C::kOnce>(cache.k_codes + r * row_bytes + vec * 16, sb + j * 1024);
+          load_lds<C::kOnce>(cache.v_codes + r * row_bytes + vec * 16, sb + C::kV + j * 1024);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2 * (C::SW + 1); ++i) {
+      if (i % C::W != wave) continue;
+      const int half = i & 1, what = i >> 1;
+      const int64_t r = half ? r1 : r0;
+      if (what < C::SW)
+        __builtin_amdgcn_global_load_lds((gptr_t)(cache.k_scales + r * (4 * C::SW) + what * 4),
+                                         (lptr_t)(sb + C::kKS + what * KT * 4 + half * 256), 4, 0, 0);
+      else
+        __builtin_amdgcn_global_load_lds((gptr_t)(cache.v_scales + r),
+                                         (lptr_t)(sb + C::kVS + half * 256), 4, 0, 0);
+    }
+  };
+
+  f32x4 o[OT];
+  float m = -INFINITY, l = 0.0f;
+  const float c = a.scale * kLog2e;
+#pragma unroll
+  for (int t = 0; t < OT; ++t) o[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+  // Operand reads.  Keys: lane's row of 16, its 32 channels.  Values: a transposed
+  // read gives lane n of 16 channel n of 16 rows, of which lane n fetches the n-th.
+  // The pieces of a lane's weights alternate between its 16 results of the lower and
+  // of the upper 64 positions (even and odd terms), so the 16 rows of the first read
+  // are 4 g + {0 .. 3} + {0, 16} of both halves in turn, of the second 32 further on.
+  const int krow = lane & 15;
+  const int kgroup = D == 64 ? g & 1 : g;
+  const int koff = krow * ROW + ((kgroup ^ swz_q4<D>(krow)) << 4);
+  const int ksoff = krow * 4 + kgroup;
+  const int n16 = lane & 15;
+  const int vkey = 64 * (n16 & 1) + 16 * (n16 >> 3) + 4 * g + ((n16 >> 1) & 3);
+  const int voff = vkey * ROW + (swz_q4<D>(vkey) << 4);
+
+  auto compute = [&](const char* sb, int u, uint64_t page0, uint64_t page1) {
+    f32x4 st[8];
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      st[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int hf = 0; hf < HALVES; ++hf) {
+        const u32x4 k = *reinterpret_cast<const u32x4*>(sb + (koff ^ (hf << 6)) + t * 16 * ROW);
+        int ks = static_cast<uint8_t>(sb[C::kKS + hf * KT * 4 + ksoff + t * 64]);
+        if (C::kPad && (hf * 4 + kgroup) * 32 >= dim) ks = 0;
+#pragma unroll
+        for (int s = 0; s < QS; ++s) st[t] = mma_q4(k, ks, qf[hf][s], qs[hf][s], st[t]);
+      }
+    }
+    // bit 4 t + r: position 16 t + r (and the lane's part 4 g) is not seen
+    uint32_t dead = 0;
+    if (u * KT + KT - 1 > all_hi || u * KT < all_lo) {
+      // a row that sees nothing has span 0 at a position that is none
+      const int d = u * KT + 4 * g - see_lo;
+#pragma unroll
+      for (int t = 0; t < 8; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          dead |= (static_cast<uint32_t>(d + t * 16 + r) > see_span ? 1u : 0u) << (4 * t + r);
+    }
+    if ((page0 & page1) != ~uint64_t{0}) {
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        const uint32_t here = static_cast<uint32_t>((t < 4 ? page0 : page1) >> (16 * (t & 3) + 4 * g));
+        dead |= (~here & 15u) << (4 * t);
+      }
+    }
+    const bool masked = __any(dead != 0);
+    if (masked) {
+#pragma unroll
+      for (int t = 0; t < 8; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) st[t][r] = (dead >> (4 * t + r)) & 1 ? -INFINITY : st[t][r];
+    }
+    float mx = st[0][0];
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) mx = fmaxf(mx, st[t][r]);
+    mx = max_across<16>(mx);
+    mx = max_across<32>(mx);
+    // the reference lies kSlack above the largest score where it moves, and moves
+    // when a score reaches it: weights are 1 and less
+    const bool move = mx * c > m;      // m = -inf: any score moves it
+    if (__any(move)) {
+      const float mn = move ? mx * c + kSlack : m;
+      const float f = __builtin_amdgcn_exp2f(m - (mn == -INFINITY ? 0.0f : mn));
+      m = mn;
+      l *= f;
+#pragma unroll
+      for (int t = 0; t < OT; ++t) o[t] *= f;
+    }
+    const float ref = m == -INFINITY ? 0.0f : m;
+    float sum = 0.0f;
+    f32x16 x0, x1;       // weights times scales: of the lower 64 positions, of the upper
+    uint32_t top = 0;
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      f32x4 vs = *reinterpret_cast<const f32x4*>(sb + C::kVS + (t * 16 + 4 * g) * 4);
+      if (masked) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) vs[r] = (dead >> (4 * t + r)) & 1 ? 0.0f : vs[r];
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float p = __builtin_amdgcn_exp2f(fmaf(st[t][r], c, -ref));
+        sum += p;
+        const float w = p * vs[r];
+        top = max(top, __float_as_uint(w));
+        if (t < 4) x0[t * 4 + r] = w;
+        else x1[(t - 4) * 4 + r] = w;
+      }
+    }
+    l += sum;
+    u32x6 piece[PP];
+    int scale[PP];
+    split_pieces<PP>(x0, x1, top, piece, scale);
+    const int vo = fresh(voff);
+#pragma unroll
+    for (int t = 0; t < OT; ++t) {
+      typedef __attribute__((address_space(3))) i32x2* tr_t;
+      const char* p = sb + C::kV + (vo ^ (t * 8));
+      const i32x2 y0 = __builtin_amdgcn_ds_read_tr4_b64_v2i32((tr_t)(p));
+      const i32x2 y1 = __builtin_amdgcn_ds_read_tr4_b64_v2i32((tr_t)(p + 32 * ROW));
+      const u32x4 v = {static_cast<uint32_t>(y0.x), static_cast<uint32_t>(y0.y),
+                       static_cast<uint32_t>(y1.x), static_cast<uint32_t>(y1.y)};
+#pragma unroll
+      for (int s = 0; s < PP; ++s) o[t] = mma_q4(v, 127, piece[s], scale[s], o[t]);
+    }
+  };
+
+  const int n_units = it.u1 - it.u0;
+  if (n_units > 0) {
+    // Step n computes unit n from buffer n % 2 while unit n + 1 is under way.  Loads
+    // past the last unit read its nearest position again.  The table entries of turn
+    // q (units 2 q, 2 q + 1) are loaded into LDS as well, one turn before their use.
+    if (C::kPad) {
+      // (vectors that a row does not have are loaded by no one: zero from here on)
+      for (int i = tid; i < C::kKS / 16; i += C::W * kWave) {
+        reinterpret_cast<u32x4*>(sb0)[i] = u32x4{0, 0, 0, 0};
+        reinterpret_cast<u32x4*>(sb1)[i] = u32x4{0, 0, 0, 0};
+      }
+      __syncthreads();
+    }
+    char* const ring[2] = {sb0, sb1};
+    const int first = it.u0 * KT;
+    int32_t* const ids = sid + wave * C::SUPER;
+    int64_t off[IDS];
+    uint64_t mask[IDS], mask_next[IDS];
+    auto look = [&](int q) {          // starts the lookups of turn q
+#pragma unroll
+      for (int i = 0; i < IDS; ++i)
+        __builtin_amdgcn_global_load_lds((gptr_t)entry(first + q * C::SUPER + i * kWave),
+                                         (lptr_t)(ids + i * kWave), 4, 0, 0);
+    };
+    auto turn = [&](int q) {          // turn q, looked up, becomes the one that loads
+#pragma unroll
+      for (int i = 0; i < IDS; ++i) {
+        const int id = ids[i * kWave + lane];
+        mask_next[i] = paged(id);
+        off[i] = row_of(first + q * C::SUPER + i * kWave, id);
+      }
+    };
+    look(0);
+    wait_loads();
+    turn(0);
+    wait_loads();                     // the entries are read before the next overwrite them
+    look(1);
+    load_unit(first, off[0], off[1], ring[0]);
+    for (int n = 0; n < n_units; n += 2) {
+      wait_loads();
+      __builtin_amdgcn_s_barrier();
+#pragma unroll
+      for (int i = 0; i < IDS; ++i) mask[i] = mask_next[i];
+      load_unit(first + (n + 1) * KT, off[2], off[3], ring[1]);
+      compute(ring[0], it.u0 + n, mask[0], mask[1]);
+      wait_loads();
+      __builtin_amdgcn_s_barrier();
+      turn(n / 2 + 1);
+      load_unit(first + (n + 2) * KT, off[0], off[1], ring[0]);
+      look(n / 2 + 2);
+      if (n + 1 < n_units) compute(ring[1], it.u0 + n + 1, mask[2], mask[3]);
+    }
+    // no load may still be under way when the workgroup gives its LDS back
+    wait_loads();
+    __syncthreads();
+  }
+  l += __shfl_xor(l, 16, kWave);
+  l += __shfl_xor(l, 32, kWave);
+  if (row < it.rows && g == 0) {
+    if (it.splits > 1) {
+      const int64_t p = (static_cast<int64_t>(it.slot) * a.kv_heads + h) * C::MT + row;
+      a.part_ml[p * 2] = m;
+      a.part_ml[p * 2 + 1] = l;
+    } else if (a.lse) {
+      int token, head;
+      attend_row(a, it.token0, it.row0 + fresh(row), h, token, head);
+      a.lse[static_cast<int64_t>(token) * a.heads + head] =
+          l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+    }
+  }
+  if (it.splits > 1) {
+    if (row < it.rows) {
+      const int64_t p = (static_cast<int64_t>(it.slot) * a.kv_heads + h) * C::MT + row;
+      float* po = a.part_o + p * dim + 4 * g;
+#pragma unroll
+      for (int t = 0; t < OT; ++t)
+        if (!C::kPad || t * 16 < dim) *reinterpret_cast<f32x4*>(po + t * 16) = o[t];
+    }
+    return;
+  }
+  // whole output rows: turned in LDS (each wavefront its 16 rows), then 16 bytes a lane
+  static_assert(4 * 16 * D * 2 <= C::BYTES, "the rows of four wavefronts fit a buffer");
+  char* const turned = (wave < 4 ? sb0 : sb1) + (wave & 3) * 16 * D * 2;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const bool none = l == 0.0f;
+  const int mine = lane & 15;
+#pragma unroll
+  for (int t = 0; t < OT; ++t) {
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    const int e = t * 16 + 4 * g;
+    const f32x4 y = none ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : o[t] * inv;
+    *reinterpret_cast<u32x2*>(turned + mine * (D * 2) + (((e >> 3) ^ swz_k<D>(mine)) << 4) +
+                              (e & 4) * 2) = u32x2{pack2<T>(y[0], y[1]), pack2<T>(y[2], y[3])};
+  }
+  constexpr int OV = D / 8, PER = kWave / OV;   // vectors of an output row, rows a pass
+#pragma unroll
+  for (int i = 0; i < 16 / PER; ++i) {
+    const int r = i * PER + lane / OV, slot = lane & (OV - 1);
+    const u32x4 w = *reinterpret_cast<const u32x4*>(turned + r * (D * 2) + ((slot ^ swz_k<D>(r)) << 4));
+    if (wave * 16 + r < it.rows && (!C::kPad || slot * 8 < dim)) {
+      int token, head;
+      attend_row(a, it.token0, it.row0 + wave * 16 + r, h, token, head);
+      T* po = static_cast<T*>(a.out) + (static_cast<int64_t>(token) * a.heads + head) * dim;
+      reinterpret_cast<u32x4*>(po)[slot] = w;
+    }
+  }
+}
+
+template <class C>
+void launch_q4_cfg(const AttendArgs& a, const Q4Cache& c, hipStream_t st) {
+  hipLaunchKernelGGL(attend_q4_kernel<C>, dim3(static_cast<unsigned>(a.grid_items) * a.kv_heads),
+                     dim3(C::W * kWave), 0, st, a, c);
+}
+
+template <typename T, int D, bool kPad>
+hipError_t launch_q4_rows(const AttendArgs& a, const Q4Cache& c, int mt, hipStream_t st) {
+  switch (mt) {
+    case 16: launch_q4_cfg<Q4Cfg<T, D, kPad, 1>>(a, c, st); break;
+    case 32: launch_q4_cfg<Q4Cfg<T, D, kPad, 2>>(a, c, st); break;
+    case 48: launch_q4_cfg<Q4Cfg<T, D, kPad, 3>>(a, c, st); break;
+    case 64: launch_q4_cfg<Q4Cfg<T, D, kPad, 4>>(a, c, st); break;
+    case 128: launch_q4_cfg<Q4Cfg<T, D, kPad, 8>>(a, c, st); break;
+    default: return hipErrorInvalidValue;
+  }
+  return hipGetLastError();
+}
+
+template <int D>
+hipError_t launch_q4_width(const AttendArgs& a, const Q4Cache& c, int dtype, int mt, hipStream_t st) {
+  if (dtype == kBF16)
+    return a.D == D ? launch_q4_rows<__bf16, D, false>(a, c, mt, st)
+                    : launch_q4_rows<__bf16, D, true>(a, c, mt, st);
+  return a.D == D ? launch_q4_rows<_Float16, D, false>(a, c, mt, st)
+                  : launch_q4_rows<_Float16, D, true>(a, c, mt, st);
+}
+
+}  // namespace sv

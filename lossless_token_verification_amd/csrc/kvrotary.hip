@@ -1,0 +1,35 @@
+// Cache append with the position rotation on the way: queries turned to q_out,
+// keys turned and values as they are to their slots.  One pass over the rows, bound
+// by memory; a thread takes a vector, or the two vectors of a half-split head that
+// turn into each other.
+#include "kvrotary.h"
+
+namespace sv {
+
+namespace {
+
+template <typename T, int VEC>
+__global__ __launch_bounds__(kRotaryThreads) void rotary_kernel(RotaryArgs a, uint32_t total) {
+  const uint32_t i = blockIdx.x * kRotaryThreads + threadIdx.x;
+  if (i < total) rotary_unit<T, VEC>(a, i);
+}
+
+}  // namespace
+
+hipError_t launch_rotary(const RotaryArgs& a, int dtype, bool wide, hipStream_t st) {
+  const uint32_t total = static_cast<uint32_t>(a.T) * a.token_units;
+  const dim3 grid((total + kRotaryThreads - 1) / kRotaryThreads), block(kRotaryThreads);
+  if (dtype == kF32) {
+    if (wide) hipLaunchKernelGGL((rotary_kernel<float, 4>), grid, block, 0, st, a, total);
+    else hipLaunchKernelGGL((rotary_kernel<float, 1>), grid, block, 0, st, a, total);
+  } else if (dtype == kBF16) {
+    if (wide) hipLaunchKernelGGL((rotary_kernel<__bf16, 8>), grid, block, 0, st, a, total);
+    else hipLaunchKernelGGL((rotary_kernel<__bf16, 1>), grid, block, 0, st, a, total);
+  } else {
+    if (wide) hipLaunchKernelGGL((rotary_kernel<_Float16, 8>), grid, block, 0, st, a, total);
+    else hipLaunchKernelGGL((rotary_kernel<_Float16, 1>), grid, block, 0, st, a, total);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace sv
