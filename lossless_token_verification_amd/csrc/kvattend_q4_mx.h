@@ -46,19 +46,24 @@ __device__ __forceinline__ f32x4 mma_q4(u32x4 codes, int code_scale, u32x6 piece
 }
 
 // The N pieces of 32 numbers, even ones in x0 and odd ones in x1, the largest of
-// magnitude `top` (as bits).  The conversions read their sources while they write, so
-// their sources have to outlive them: the empty statements keep the registers apart.
-// Numbers below 2^-104 lose bits (the last piece's scale is 2^-118 at least).
+// magnitude `top` (as bits).  add: what the scales' exponents are raised by.  Two
+// pieces are scaled so that the largest is in (3.75, 7.5], more so that it is in [2, 4).
+// The conversions read their sources while they write, so their sources have to
+// outlive them: the empty statements keep the registers apart.  Numbers below 2^-104
+// lose bits (the last piece's scale is 2^-118 at least).
 template <int N>
-__device__ __forceinline__ void split_pieces(f32x16 x0, f32x16 x1, uint32_t top, u32x6 (&piece)[N],
-                                             int (&scale)[N]) {
-  const int b = max(static_cast<int>(top >> 23), 25) - 1;
+__device__ __forceinline__ void split_pieces(f32x16 x0, f32x16 x1, uint32_t top, int add,
+                                             u32x6 (&piece)[N], int (&scale)[N]) {
+#pragma clang fp contract(off)
+  const int e = N == 2 ? static_cast<int>((top + 0xfffffu) >> 23) - 2 : static_cast<int>(top >> 23) - 1;
+  const int b = max(e, 24);
 #pragma unroll
   for (int p = 0; p < N; ++p) {
     const float s = __uint_as_float(static_cast<uint32_t>(min(b, 254) - 5 * p) << 23);
     piece[p] = __builtin_amdgcn_cvt_scalef32_2xpk16_fp6_f32(x0, x1, s);
     asm volatile("" : "+v"(piece[p]) : "v"(x0), "v"(x1), "v"(s));
-    scale[p] = b >= 254 ? 255 : b - 5 * p;     // infinity or NaN among them: NaN
+    // infinity or NaN among them: NaN
+    scale[p] = top >= 0x7f800000u || b + add > 254 ? 255 : max(b + add - 5 * p, 0);
     if (p + 1 < N) {
       f32x32 y = __builtin_amdgcn_cvt_scalef32_pk32_f32_fp6(piece[p], s);
       asm volatile("" : "+v"(y) : "v"(piece[p]), "v"(s));
@@ -69,6 +74,13 @@ __device__ __forceinline__ void split_pieces(f32x16 x0, f32x16 x1, uint32_t top,
       }
     }
   }
+}
+
+// Waits for the wavefront's LDS reads, not for its loads under way.
+__device__ __forceinline__ void wait_entries() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xc07f);     // vector memory 63, LDS 0
+  asm volatile("" ::: "memory");
 }
 
 template <typename T_, int D_, bool kPad_, int W_>
@@ -89,7 +101,8 @@ struct Q4Cfg {
   static constexpr int kV = KT * ROW, kKS = 2 * kV;        // bytes: V codes, key scales,
   static constexpr int kVS = kKS + SW * KT * 4;            //   value scales
   static constexpr int BYTES = kVS + KT * 4;
-  static constexpr int SUPER = 2 * KT, IDS = SUPER / kWave;
+  static constexpr int CHUNKS = (LOADS + W - 1) / W;       // loads of a wavefront
+  static constexpr int IDS = (CHUNKS * RPL + kWave - 1) / kWave;   // its lookups, per unit
   static constexpr int OT = D / 16;                        // result tiles
   static constexpr bool kOnce = MT <= 64;                  // as in the 16-bit kernel
 };
@@ -103,14 +116,15 @@ __device__ __forceinline__ int swz_q4(int r) {
 }
 
 template <class C>
-__global__ __launch_bounds__((C::W > 4 ? C::W : 4) * kWave) __attribute__((amdgpu_waves_per_eu(C::D == 256 && C::W <= 4 ? 1 : 2))) void
+__global__ __launch_bounds__((C::W > 4 ? C::W : 4) * kWave) __attribute__((amdgpu_waves_per_eu(2))) void
 attend_q4_kernel(AttendArgs a, Q4Cache cache) {
   using T = typename C::T;
   constexpr int D = C::D, KT = C::KT, ROW = C::ROW, NV = C::NV, RPL = C::RPL, OT = C::OT;
-  constexpr int IDS = C::IDS, HALVES = C::HALVES, QS = C::QS, PQ = C::PQ, PP = C::PP;
+  constexpr int IDS = C::IDS, CHUNKS = C::CHUNKS, HALVES = C::HALVES, QS = C::QS, PQ = C::PQ, PP = C::PP;
   // (two LDS objects: a direct load into one is known to leave the other alone)
   __shared__ __attribute__((aligned(1024))) char sb0[C::BYTES], sb1[C::BYTES];
-  __shared__ __attribute__((aligned(256))) int32_t sid[C::W * C::SUPER];
+  __shared__ __attribute__((aligned(256))) int32_t sid[C::W * IDS * kWave];
+  __shared__ int32_t missing[4];   // unit + 1 where a page of the unit is missing
   __shared__ AttendPlanShared<C::W> plan;
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -136,6 +150,10 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
     const int key_first = a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
     see_lo = key_last >= key_first ? key_first : INT32_MAX;
     see_span = key_last >= key_first ? key_last - key_first : 0;
+    // scores in log2 units: the factor's significand goes into the queries, its
+    // exponent into their scales
+    int factor_exp;
+    const float factor = frexpf(a.scale * kLog2e, &factor_exp);
     const T* qr = static_cast<const T*>(a.q) + token * a.q_stride + static_cast<int64_t>(head) * dim;
 #pragma unroll
     for (int hf = 0; hf < HALVES; ++hf) {
@@ -150,15 +168,15 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
         const t8 v = __builtin_bit_cast(t8, w);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          x0[i * 4 + j] = static_cast<float>(v[2 * j]);
-          x1[i * 4 + j] = static_cast<float>(v[2 * j + 1]);
+          x0[i * 4 + j] = static_cast<float>(v[2 * j]) * factor;
+          x1[i * 4 + j] = static_cast<float>(v[2 * j + 1]) * factor;
           top = max(top, __float_as_uint(x0[i * 4 + j]) & 0x7fffffffu);
           top = max(top, __float_as_uint(x1[i * 4 + j]) & 0x7fffffffu);
         }
       }
       u32x6 piece[PQ];
       int scale[PQ];
-      split_pieces<PQ>(x0, x1, top, piece, scale);
+      split_pieces<PQ>(x0, x1, top, factor_exp, piece, scale);
 #pragma unroll
       for (int s = 0; s < QS; ++s) {
         qf[hf][s] = piece[D == 64 ? 2 * s : s];
@@ -178,69 +196,106 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
   const int32_t* table = a.table + static_cast<int64_t>(it.b) * a.max_blocks;
   const int64_t head_rows = static_cast<int64_t>(h) * a.block_size;
   const int64_t block_rows = static_cast<int64_t>(a.kv_heads) * a.block_size;
-  // Lane l looks up position base + l: its row number in the cache, and whether there
-  // is such a page.  Positions outside the item's range read the nearest one inside
-  // (and are masked); a missing page reads block 0.
-  auto nearest = [&](int base) { return min(max(base + lane, it.key_lo), it.key_hi - 1); };
-  auto entry = [&](int base) { return table + fast_div(nearest(base), a.bs); };
-  auto row_of = [&](int base, int id) -> int64_t {
-    const int key = nearest(base);
-    const int r = key - fast_div(key, a.bs) * a.block_size;
-    const int safe = id >= 0 && id < a.num_blocks ? id : 0;
-    return safe * block_rows + head_rows + r;
+  // A unit's rows are loaded RPL at a time, load j by wavefront j % W.  Lane l looks up
+  // the l-th row of its wavefront's loads (and the 64 + l-th): its row number in the
+  // cache, and whether there is such a page.  Positions outside the item's range read
+  // the nearest one inside (and are masked); a missing page reads block 0.
+  auto in_unit = [&](int i) {       // position in the unit of the wavefront's row i * 64 + lane
+    const int r = i * kWave + lane;
+    return ((r / RPL) * C::W + wave) * RPL + r % RPL;
   };
-  auto paged = [&](int id) -> uint64_t { return __ballot(id >= 0 && id < a.num_blocks); };
-
-  // Loads the unit at position `base` into LDS; r0, r1: row numbers of its halves of
-  // 64 positions.  Inside the item's range, with whole pages of rows, a load's address
-  // is one lane's row plus a lane constant and moves through scalar registers.
+  auto nearest = [&](int key) { return min(max(key, it.key_lo), it.key_hi - 1); };
+  auto paged = [&](int id) { return id >= 0 && id < a.num_blocks; };
+  int32_t* const ids = sid + wave * (IDS * kWave);
+  auto look = [&](int base) {       // starts the lookups of the unit at position `base`
+#pragma unroll
+    for (int i = 0; i < IDS; ++i)
+      __builtin_amdgcn_global_load_lds((gptr_t)(table + fast_div(nearest(base + in_unit(i)), a.bs)),
+                                       (lptr_t)(ids + i * kWave), 4, 0, 0);
+  };
+  int64_t off[IDS];
+  auto turn = [&](int n, int base) {    // the unit looked up (the n-th) becomes the next to load
+#pragma unroll
+    for (int i = 0; i < IDS; ++i) {
+      const int id = ids[i * kWave + lane];
+      const int key = nearest(base + in_unit(i));
+      off[i] = (paged(id) ? id : 0) * block_rows + head_rows + key - fast_div(key, a.bs) * a.block_size;
+      if (__any(!paged(id) && in_unit(i) < KT)) missing[n & 3] = n + 1;
+    }
+  };
+  // Loads the unit at position `base` into LDS.  Inside the item's range, with whole
+  // pages of rows, a load's address is one lane's row plus a lane constant and moves
+  // through scalar registers.
   const int lq = lane / NV, lslot = lane & (NV - 1);
   const bool whole_rows = a.block_size % RPL == 0;
-  auto load_unit = [&](int base, int64_t r0, int64_t r1, char* sb) {
+  auto load_unit = [&](int base, char* sb) {
     const bool inside = whole_rows && base >= it.key_lo && base + KT <= it.key_hi;
 #pragma unroll
-    for (int i = 0; i < (C::LOADS + C::W - 1) / C::W; ++i) {
+    for (int i = 0; i < CHUNKS; ++i) {
       const int j = wave + i * C::W;                 // which RPL rows
       if (C::LOADS % C::W != 0 && j >= C::LOADS) break;
-      const int from = j * RPL & (kWave - 1);
-      const bool upper = j * RPL >= kWave;
-      const int64_t mine = upper ? r1 : r0;
+      const int from = i * RPL & (kWave - 1);
+      const int64_t mine = off[i * RPL / kWave];
       const int vec = lslot ^ swz_q4<D>(j * RPL + lq);
+      int64_t r;
       if (inside) {
-        const int lo = static_cast<int>(mine), hi = static_cast<int>(mine >> 32);
-        const uint32_t s0 = __builtin_amdgcn_readlane(lo, from);
-        const uint32_t s1 = __builtin_amdgcn_readlane(hi, from);
-        const int64_t r = static_cast<int64_t>((static_cast<uint64_t>(s1) << 32) | s0);
+        const uint32_t s0 = __builtin_amdgcn_readlane(static_cast<int>(mine), from);
+        const uint32_t s1 = __builtin_amdgcn_readlane(static_cast<int>(mine >> 32), from);
+        r = static_cast<int64_t>((static_cast<uint64_t>(s1) << 32) | s0);
         const uint32_t in = lq * row_bytes + vec * 16;
         if (!C::kPad || vec * 16 < row_bytes) {
           load_lds<C::kOnce>(cache.k_codes + r * row_bytes + in, sb + j * 1024);
           load_lds<C::kOnce>(cache.v_codes + r * row_bytes + in, sb + C::kV + j * 1024);
         }
+        asm volatile("; scalar addresses");   // keeps the two forms from being merged
       } else {
-        const int64_t r = __shfl(static_cast<long long>(mine), from + lq, kWave);
+        r = __shfl(static_cast<long long>(mine), from + lq, kWave);
         if (!C::kPad || vec * 16 < row_bytes) {
           load_lds<C::kOnce>(cache.k_codes + r * row_bytes + vec * 16, sb + j * 1024);
           load_lds<C::kOnce>(cache.v_codes + r * row_bytes + vec * 16, sb + C::kV + j * 1024);
         }
       }
     }
+    // the scales of the same rows, a run of RPL lanes for each load
+    if (C::W <= C::LOADS || wave < C::LOADS) {
 #pragma unroll
-    for (int i = 0; i < 2 * (C::SW + 1); ++i) {
-      if (i % C::W != wave) continue;
-      const int half = i & 1, what = i >> 1;
-      const int64_t r = half ? r1 : r0;
-      if (what < C::SW)
-        __builtin_amdgcn_global_load_lds((gptr_t)(cache.k_scales + r * (4 * C::SW) + what * 4),
-                                         (lptr_t)(sb + C::kKS + what * KT * 4 + half * 256), 4, 0, 0);
-      else
-        __builtin_amdgcn_global_load_lds((gptr_t)(cache.v_scales + r),
-                                         (lptr_t)(sb + C::kVS + half * 256), 4, 0, 0);
+      for (int i = 0; i < IDS; ++i) {
+        if constexpr (C::W == 1) {          // rows in order: 64 at a time
+#pragma unroll
+          for (int w = 0; w < C::SW; ++w)
+            __builtin_amdgcn_global_load_lds((gptr_t)(cache.k_scales + off[i] * (4 * C::SW) + w * 4),
+                                             (lptr_t)(sb + C::kKS + w * KT * 4 + i * 256), 4, 0, 0);
+          __builtin_amdgcn_global_load_lds((gptr_t)(cache.v_scales + off[i]),
+                                           (lptr_t)(sb + C::kVS + i * 256), 4, 0, 0);
+        } else {
+          // (lane l of a load writes to its base + 4 l: the base that puts lane
+          // c RPL at row j RPL)
+#pragma unroll
+          for (int c = 0; c < kWave / RPL && i * (kWave / RPL) + c < CHUNKS; ++c) {
+            const int j = wave + (i * (kWave / RPL) + c) * C::W;
+            if (C::LOADS % C::W != 0 && j >= C::LOADS) break;
+            const int to = (j - c) * RPL * 4;
+            if (lane / RPL == c) {
+#pragma unroll
+              for (int w = 0; w < C::SW; ++w)
+                __builtin_amdgcn_global_load_lds(
+                    (gptr_t)(cache.k_scales + off[i] * (4 * C::SW) + w * 4),
+                    (lptr_t)(sb + C::kKS + w * KT * 4 + to), 4, 0, 0);
+              __builtin_amdgcn_global_load_lds((gptr_t)(cache.v_scales + off[i]),
+                                               (lptr_t)(sb + C::kVS + to), 4, 0, 0);
+            }
+          }
+        }
+      }
     }
   };
 
+  // The scores come out less the reference of their row (they start from its
+  // negative): 0 until the row sees a position, then kSlack above the largest score
+  // where it moved last, so that weights are 1 and less.  It moves when a score
+  // exceeds it.  seen: -inf before the row sees a position, 0 after.
   f32x4 o[OT];
-  float m = -INFINITY, l = 0.0f;
-  const float c = a.scale * kLog2e;
+  float ref = 0.0f, seen = -INFINITY, l = 0.0f;
 #pragma unroll
   for (int t = 0; t < OT; ++t) o[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
@@ -257,23 +312,31 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
   const int vkey = 64 * (n16 & 1) + 16 * (n16 >> 3) + 4 * g + ((n16 >> 1) & 3);
   const int voff = vkey * ROW + (swz_q4<D>(vkey) << 4);
 
-  auto compute = [&](const char* sb, int u, uint64_t page0, uint64_t page1) {
+  // Unit u, the n-th of the item.
+  auto compute = [&](const char* sb, int u, int n) {
     f32x4 st[8];
 #pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      st[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int hf = 0; hf < HALVES; ++hf) {
+      u32x4 k[8];
+      int ks[8];
 #pragma unroll
-      for (int hf = 0; hf < HALVES; ++hf) {
-        const u32x4 k = *reinterpret_cast<const u32x4*>(sb + (koff ^ (hf << 6)) + t * 16 * ROW);
-        int ks = static_cast<uint8_t>(sb[C::kKS + hf * KT * 4 + ksoff + t * 64]);
-        if (C::kPad && (hf * 4 + kgroup) * 32 >= dim) ks = 0;
-#pragma unroll
-        for (int s = 0; s < QS; ++s) st[t] = mma_q4(k, ks, qf[hf][s], qs[hf][s], st[t]);
+      for (int t = 0; t < 8; ++t) {
+        k[t] = *reinterpret_cast<const u32x4*>(sb + (koff ^ (hf << 6)) + t * 16 * ROW);
+        ks[t] = static_cast<uint8_t>(sb[C::kKS + hf * KT * 4 + ksoff + t * 64]);
+        if (C::kPad && (hf * 4 + kgroup) * 32 >= dim) ks[t] = 0;
       }
+#pragma unroll
+      for (int s = 0; s < QS; ++s)
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+          st[t] = mma_q4(k[t], ks[t], qf[hf][s], qs[hf][s],
+                         hf == 0 && s == 0 ? f32x4{-ref, -ref, -ref, -ref} : st[t]);
     }
-    // bit 4 t + r: position 16 t + r (and the lane's part 4 g) is not seen
+    // Positions that are not seen, bit 4 t + r: 16 t + r and the lane's part 4 g.
+    const bool gone = missing[n & 3] == n + 1;
+    const bool masked = u * KT + KT - 1 > all_hi || u * KT < all_lo || gone;
     uint32_t dead = 0;
-    if (u * KT + KT - 1 > all_hi || u * KT < all_lo) {
+    if (masked) {
       // a row that sees nothing has span 0 at a position that is none
       const int d = u * KT + 4 * g - see_lo;
 #pragma unroll
@@ -281,16 +344,15 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
 #pragma unroll
         for (int r = 0; r < 4; ++r)
           dead |= (static_cast<uint32_t>(d + t * 16 + r) > see_span ? 1u : 0u) << (4 * t + r);
-    }
-    if ((page0 & page1) != ~uint64_t{0}) {
+      if (gone) {
+        const int b0 = u * KT + lane;
+        const uint64_t page0 = __ballot(paged(table[fast_div(nearest(b0), a.bs)]));
+        const uint64_t page1 = __ballot(paged(table[fast_div(nearest(b0 + kWave), a.bs)]));
 #pragma unroll
-      for (int t = 0; t < 8; ++t) {
-        const uint32_t here = static_cast<uint32_t>((t < 4 ? page0 : page1) >> (16 * (t & 3) + 4 * g));
-        dead |= (~here & 15u) << (4 * t);
+        for (int t = 0; t < 8; ++t)
+          dead |= (~static_cast<uint32_t>((t < 4 ? page0 : page1) >> (16 * (t & 3) + 4 * g)) & 15u)
+                  << (4 * t);
       }
-    }
-    const bool masked = __any(dead != 0);
-    if (masked) {
 #pragma unroll
       for (int t = 0; t < 8; ++t)
 #pragma unroll
@@ -303,107 +365,106 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
       for (int r = 0; r < 4; ++r) mx = fmaxf(mx, st[t][r]);
     mx = max_across<16>(mx);
     mx = max_across<32>(mx);
-    // the reference lies kSlack above the largest score where it moves, and moves
-    // when a score reaches it: weights are 1 and less
-    const bool move = mx * c > m;      // m = -inf: any score moves it
-    if (__any(move)) {
-      const float mn = move ? mx * c + kSlack : m;
-      const float f = __builtin_amdgcn_exp2f(m - (mn == -INFINITY ? 0.0f : mn));
-      m = mn;
+    if (__any(mx > seen)) {
+      const float up = mx > seen ? mx + kSlack : 0.0f;
+      const float f = __builtin_amdgcn_exp2f(seen - up);    // (nothing to keep before: 0)
+      seen = mx > seen ? 0.0f : seen;
+      ref += up;
       l *= f;
 #pragma unroll
       for (int t = 0; t < OT; ++t) o[t] *= f;
+#pragma unroll
+      for (int t = 0; t < 8; ++t) st[t] -= up;
     }
-    const float ref = m == -INFINITY ? 0.0f : m;
     float sum = 0.0f;
     f32x16 x0, x1;       // weights times scales: of the lower 64 positions, of the upper
     uint32_t top = 0;
+    {
+#pragma clang fp contract(off)
 #pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      f32x4 vs = *reinterpret_cast<const f32x4*>(sb + C::kVS + (t * 16 + 4 * g) * 4);
-      if (masked) {
+      for (int t = 0; t < 8; ++t) {
+        const f32x4 vs = *reinterpret_cast<const f32x4*>(sb + C::kVS + (t * 16 + 4 * g) * 4);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) vs[r] = (dead >> (4 * t + r)) & 1 ? 0.0f : vs[r];
-      }
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float p = __builtin_amdgcn_exp2f(fmaf(st[t][r], c, -ref));
-        sum += p;
-        const float w = p * vs[r];
-        top = max(top, __float_as_uint(w));
-        if (t < 4) x0[t * 4 + r] = w;
-        else x1[(t - 4) * 4 + r] = w;
+        for (int r = 0; r < 4; ++r) {
+          const float p = __builtin_amdgcn_exp2f(st[t][r]);
+          sum += p;
+          if (t < 4) x0[t * 4 + r] = p * vs[r];
+          else x1[(t - 4) * 4 + r] = p * vs[r];
+        }
       }
     }
+    if (masked) {        // (their scales may be anything)
+      const uint32_t gone_bits = fresh(static_cast<int>(dead));
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        x0[i] = (gone_bits >> i) & 1 ? 0.0f : x0[i];
+        x1[i] = (gone_bits >> (16 + i)) & 1 ? 0.0f : x1[i];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = max(max(top, __float_as_uint(x0[i])), __float_as_uint(x1[i]));
     l += sum;
     u32x6 piece[PP];
     int scale[PP];
-    split_pieces<PP>(x0, x1, top, piece, scale);
+    split_pieces<PP>(x0, x1, top, 0, piece, scale);
     const int vo = fresh(voff);
 #pragma unroll
-    for (int t = 0; t < OT; ++t) {
-      typedef __attribute__((address_space(3))) i32x2* tr_t;
-      const char* p = sb + C::kV + (vo ^ (t * 8));
-      const i32x2 y0 = __builtin_amdgcn_ds_read_tr4_b64_v2i32((tr_t)(p));
-      const i32x2 y1 = __builtin_amdgcn_ds_read_tr4_b64_v2i32((tr_t)(p + 32 * ROW));
-      const u32x4 v = {static_cast<uint32_t>(y0.x), static_cast<uint32_t>(y0.y),
-                       static_cast<uint32_t>(y1.x), static_cast<uint32_t>(y1.y)};
+    for (int t0 = 0; t0 < OT; t0 += 4) {
+      u32x4 v[4];
 #pragma unroll
-      for (int s = 0; s < PP; ++s) o[t] = mma_q4(v, 127, piece[s], scale[s], o[t]);
+      for (int t = 0; t < 4; ++t) {
+        typedef __attribute__((address_space(3))) i32x2* tr_t;
+        const char* p = sb + C::kV + (vo ^ ((t0 + t) * 8));
+        const i32x2 y0 = __builtin_amdgcn_ds_read_tr4_b64_v2i32((tr_t)(p));
+        const i32x2 y1 = __builtin_amdgcn_ds_read_tr4_b64_v2i32((tr_t)(p + 32 * ROW));
+        v[t] = u32x4{static_cast<uint32_t>(y0.x), static_cast<uint32_t>(y0.y),
+                     static_cast<uint32_t>(y1.x), static_cast<uint32_t>(y1.y)};
+      }
+#pragma unroll
+      for (int s = 0; s < PP; ++s)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) o[t0 + t] = mma_q4(v[t], 127, piece[s], scale[s], o[t0 + t]);
     }
   };
 
   const int n_units = it.u1 - it.u0;
   if (n_units > 0) {
-    // Step n computes unit n from buffer n % 2 while unit n + 1 is under way.  Loads
-    // past the last unit read its nearest position again.  The table entries of turn
-    // q (units 2 q, 2 q + 1) are loaded into LDS as well, one turn before their use.
+    // Step n computes unit n from buffer n % 2 while unit n + 1 is under way; the
+    // table entries of unit n + 2 are turned into addresses meanwhile and those of
+    // unit n + 3 looked up, into LDS as well.  Loads past the last unit read its
+    // nearest position again.
     if (C::kPad) {
       // (vectors that a row does not have are loaded by no one: zero from here on)
       for (int i = tid; i < C::kKS / 16; i += C::W * kWave) {
         reinterpret_cast<u32x4*>(sb0)[i] = u32x4{0, 0, 0, 0};
         reinterpret_cast<u32x4*>(sb1)[i] = u32x4{0, 0, 0, 0};
       }
-      __syncthreads();
     }
-    char* const ring[2] = {sb0, sb1};
+    if (tid < 4) missing[tid] = 0;
     const int first = it.u0 * KT;
-    int32_t* const ids = sid + wave * C::SUPER;
-    int64_t off[IDS];
-    uint64_t mask[IDS], mask_next[IDS];
-    auto look = [&](int q) {          // starts the lookups of turn q
-#pragma unroll
-      for (int i = 0; i < IDS; ++i)
-        __builtin_amdgcn_global_load_lds((gptr_t)entry(first + q * C::SUPER + i * kWave),
-                                         (lptr_t)(ids + i * kWave), 4, 0, 0);
-    };
-    auto turn = [&](int q) {          // turn q, looked up, becomes the one that loads
-#pragma unroll
-      for (int i = 0; i < IDS; ++i) {
-        const int id = ids[i * kWave + lane];
-        mask_next[i] = paged(id);
-        off[i] = row_of(first + q * C::SUPER + i * kWave, id);
-      }
-    };
-    look(0);
+    look(first);
     wait_loads();
-    turn(0);
+    __syncthreads();
+    turn(0, first);
     wait_loads();                     // the entries are read before the next overwrite them
-    look(1);
-    load_unit(first, off[0], off[1], ring[0]);
+    load_unit(first, sb0);
+    look(first + KT);
+    wait_loads();
+    turn(1, first + KT);
+    wait_loads();
+    look(first + 2 * KT);
+    auto step = [&](int n, char* now, char* next) {
+      wait_loads();
+      __builtin_amdgcn_s_barrier();
+      load_unit(first + (n + 1) * KT, next);
+      turn(n + 2, first + (n + 2) * KT);
+      wait_entries();
+      look(first + (n + 3) * KT);
+      if (n < n_units) compute(now, it.u0 + n, n);
+    };
     for (int n = 0; n < n_units; n += 2) {
-      wait_loads();
-      __builtin_amdgcn_s_barrier();
-#pragma unroll
-      for (int i = 0; i < IDS; ++i) mask[i] = mask_next[i];
-      load_unit(first + (n + 1) * KT, off[2], off[3], ring[1]);
-      compute(ring[0], it.u0 + n, mask[0], mask[1]);
-      wait_loads();
-      __builtin_amdgcn_s_barrier();
-      turn(n / 2 + 1);
-      load_unit(first + (n + 2) * KT, off[0], off[1], ring[0]);
-      look(n / 2 + 2);
-      if (n + 1 < n_units) compute(ring[1], it.u0 + n + 1, mask[2], mask[3]);
+      step(n, sb0, sb1);
+      step(n + 1, sb1, sb0);
     }
     // no load may still be under way when the workgroup gives its LDS back
     wait_loads();
@@ -414,13 +475,13 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
   if (row < it.rows && g == 0) {
     if (it.splits > 1) {
       const int64_t p = (static_cast<int64_t>(it.slot) * a.kv_heads + h) * C::MT + row;
-      a.part_ml[p * 2] = m;
+      a.part_ml[p * 2] = seen == 0.0f ? ref : -INFINITY;
       a.part_ml[p * 2 + 1] = l;
     } else if (a.lse) {
       int token, head;
       attend_row(a, it.token0, it.row0 + fresh(row), h, token, head);
       a.lse[static_cast<int64_t>(token) * a.heads + head] =
-          l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+          l == 0.0f ? -INFINITY : (ref + log2f(l)) * kLn2;
     }
   }
   if (it.splits > 1) {
