@@ -136,7 +136,7 @@ sv::AttendShape q4_shape(const spec_kv_attention_desc& d) {
   const int64_t n = std::min<int64_t>(d.max_new > 0 ? d.max_new : mean, d.tokens);
   const int64_t rows = n * (d.heads / d.kv_heads);
   s.matrix = true;
-  s.mt = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 48 ? 48 : rows <= 64 ? 64 : 128;
+  s.mt = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 48 ? 48 : 64;
   s.kt = sv::kQ4KT;
   s.wgs = d.head_dim > 128 ? 512 : 1024;
   s.min_units = 1;
@@ -151,6 +151,8 @@ int32_t make_q4_plan(const spec_kv_attention_desc* d, AttendPlan* p) {
     return fail(SV_ERR_UNSUPPORTED, "head_dim must be a multiple of 32 up to %d", SV_MAX_HEAD_DIM);
   if (d->block_stride != 0)
     return fail(SV_ERR_INVALID_ARG, "block_stride must be 0: a 4-bit cache is dense");
+  if (static_cast<int64_t>(d->num_blocks) * d->block_size * d->kv_heads > UINT32_MAX)
+    return fail(SV_ERR_UNSUPPORTED, "num_blocks * block_size * kv_heads >= 2^32");
   p->shape = q4_shape(*d);
   return attend_split(d, p, p->shape.mt * 4);
 }

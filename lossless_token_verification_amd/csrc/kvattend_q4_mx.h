@@ -34,6 +34,7 @@ typedef uint32_t u32x6 __attribute__((ext_vector_type(6)));
 typedef float f32x32 __attribute__((ext_vector_type(32)));
 
 // Codes (4 bits, A) times pieces (6 bits, B), each with its scale's byte.
+template <int kByte = 0>   // of piece_scale: the piece's
 __device__ __forceinline__ f32x4 mma_q4(u32x4 codes, int code_scale, u32x6 piece, int piece_scale,
                                         f32x4 c) {
   const i32x8 x = {static_cast<int>(codes[0]), static_cast<int>(codes[1]),
@@ -41,7 +42,7 @@ __device__ __forceinline__ f32x4 mma_q4(u32x4 codes, int code_scale, u32x6 piece
   const i32x8 y = {static_cast<int>(piece[0]), static_cast<int>(piece[1]),
                    static_cast<int>(piece[2]), static_cast<int>(piece[3]),
                    static_cast<int>(piece[4]), static_cast<int>(piece[5]), 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 2, 0, code_scale, 0,
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 2, 0, code_scale, kByte,
                                                           piece_scale);
 }
 
@@ -105,6 +106,7 @@ struct Q4Cfg {
   static constexpr int IDS = (CHUNKS * RPL + kWave - 1) / kWave;   // its lookups, per unit
   static constexpr int OT = D / 16;                        // result tiles
   static constexpr bool kOnce = MT <= 64;                  // as in the 16-bit kernel
+  static constexpr int kPerSimd = D == 256 || W == 1 || (D == 128 && W == 2) ? 2 : 3;   // wavefronts
 };
 
 // LDS vector permutation of row r: vector v lies at v ^ swz(r), so that the 16 rows
@@ -116,7 +118,7 @@ __device__ __forceinline__ int swz_q4(int r) {
 }
 
 template <class C>
-__global__ __launch_bounds__((C::W > 4 ? C::W : 4) * kWave) __attribute__((amdgpu_waves_per_eu(2))) void
+__global__ __launch_bounds__((C::W > 4 ? C::W : 4) * kWave) __attribute__((amdgpu_waves_per_eu(C::kPerSimd))) void
 attend_q4_kernel(AttendArgs a, Q4Cache cache) {
   using T = typename C::T;
   constexpr int D = C::D, KT = C::KT, ROW = C::ROW, NV = C::NV, RPL = C::RPL, OT = C::OT;
@@ -141,7 +143,7 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
   int see_lo;
   uint32_t see_span;     // the positions it sees: see_span of them from see_lo on, and that one
   u32x6 qf[HALVES][QS];
-  int qs[HALVES][QS];
+  int qs[HALVES];        // a byte for each step's pieces
   {
     int token, head;
     attend_row(a, it.token0, it.row0 + min(row, it.rows - 1), h, token, head);
@@ -177,14 +179,16 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
       u32x6 piece[PQ];
       int scale[PQ];
       split_pieces<PQ>(x0, x1, top, factor_exp, piece, scale);
+      qs[hf] = 0;
 #pragma unroll
       for (int s = 0; s < QS; ++s) {
         qf[hf][s] = piece[D == 64 ? 2 * s : s];
-        qs[hf][s] = scale[D == 64 ? 2 * s : s];
+        int byte = scale[D == 64 ? 2 * s : s];
         if (D == 64 && g >= 2) {
           qf[hf][s] = piece[D == 64 ? 2 * s + 1 : s];
-          qs[hf][s] = scale[D == 64 ? 2 * s + 1 : s];
+          byte = scale[D == 64 ? 2 * s + 1 : s];
         }
+        qs[hf] |= byte << (8 * s);
       }
     }
   }
@@ -194,8 +198,9 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
   const int all_lo = a.window > 0 && pos_last >= a.window ? pos_last - a.window + 1 : 0;
 
   const int32_t* table = a.table + static_cast<int64_t>(it.b) * a.max_blocks;
-  const int64_t head_rows = static_cast<int64_t>(h) * a.block_size;
-  const int64_t block_rows = static_cast<int64_t>(a.kv_heads) * a.block_size;
+  // (rows of the cache are numbered in 32 bits)
+  const uint32_t head_rows = static_cast<uint32_t>(h) * a.block_size;
+  const uint32_t block_rows = static_cast<uint32_t>(a.kv_heads) * a.block_size;
   // A unit's rows are loaded RPL at a time, load j by wavefront j % W.  Lane l looks up
   // the l-th row of its wavefront's loads (and the 64 + l-th): its row number in the
   // cache, and whether there is such a page.  Positions outside the item's range read
@@ -213,13 +218,14 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
       __builtin_amdgcn_global_load_lds((gptr_t)(table + fast_div(nearest(base + in_unit(i)), a.bs)),
                                        (lptr_t)(ids + i * kWave), 4, 0, 0);
   };
-  int64_t off[IDS];
+  uint32_t off[IDS];
   auto turn = [&](int n, int base) {    // the unit looked up (the n-th) becomes the next to load
 #pragma unroll
     for (int i = 0; i < IDS; ++i) {
       const int id = ids[i * kWave + lane];
       const int key = nearest(base + in_unit(i));
-      off[i] = (paged(id) ? id : 0) * block_rows + head_rows + key - fast_div(key, a.bs) * a.block_size;
+      off[i] = (paged(id) ? id : 0) * block_rows + head_rows +
+               (key - fast_div(key, a.bs) * a.block_size);
       if (__any(!paged(id) && in_unit(i) < KT)) missing[n & 3] = n + 1;
     }
   };
@@ -235,24 +241,22 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
       const int j = wave + i * C::W;                 // which RPL rows
       if (C::LOADS % C::W != 0 && j >= C::LOADS) break;
       const int from = i * RPL & (kWave - 1);
-      const int64_t mine = off[i * RPL / kWave];
+      const uint32_t mine = off[i * RPL / kWave];
       const int vec = lslot ^ swz_q4<D>(j * RPL + lq);
-      int64_t r;
       if (inside) {
-        const uint32_t s0 = __builtin_amdgcn_readlane(static_cast<int>(mine), from);
-        const uint32_t s1 = __builtin_amdgcn_readlane(static_cast<int>(mine >> 32), from);
-        r = static_cast<int64_t>((static_cast<uint64_t>(s1) << 32) | s0);
-        const uint32_t in = lq * row_bytes + vec * 16;
+        const int64_t at = static_cast<int64_t>(__builtin_amdgcn_readlane(mine, from)) * row_bytes;
+        const uint32_t in = fresh(lq * row_bytes + vec * 16);
         if (!C::kPad || vec * 16 < row_bytes) {
-          load_lds<C::kOnce>(cache.k_codes + r * row_bytes + in, sb + j * 1024);
-          load_lds<C::kOnce>(cache.v_codes + r * row_bytes + in, sb + C::kV + j * 1024);
+          load_lds<C::kOnce>(cache.k_codes + at + in, sb + j * 1024);
+          load_lds<C::kOnce>(cache.v_codes + at + in, sb + C::kV + j * 1024);
         }
         asm volatile("; scalar addresses");   // keeps the two forms from being merged
       } else {
-        r = __shfl(static_cast<long long>(mine), from + lq, kWave);
+        const uint32_t r = __shfl(mine, from + lq, kWave);
+        const int64_t at = static_cast<int64_t>(r) * row_bytes + fresh(vec * 16);
         if (!C::kPad || vec * 16 < row_bytes) {
-          load_lds<C::kOnce>(cache.k_codes + r * row_bytes + vec * 16, sb + j * 1024);
-          load_lds<C::kOnce>(cache.v_codes + r * row_bytes + vec * 16, sb + C::kV + j * 1024);
+          load_lds<C::kOnce>(cache.k_codes + at, sb + j * 1024);
+          load_lds<C::kOnce>(cache.v_codes + at, sb + C::kV + j * 1024);
         }
       }
     }
@@ -263,7 +267,7 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
         if constexpr (C::W == 1) {          // rows in order: 64 at a time
 #pragma unroll
           for (int w = 0; w < C::SW; ++w)
-            __builtin_amdgcn_global_load_lds((gptr_t)(cache.k_scales + off[i] * (4 * C::SW) + w * 4),
+            __builtin_amdgcn_global_load_lds((gptr_t)(cache.k_scales + static_cast<int64_t>(off[i]) * (4 * C::SW) + w * 4),
                                              (lptr_t)(sb + C::kKS + w * KT * 4 + i * 256), 4, 0, 0);
           __builtin_amdgcn_global_load_lds((gptr_t)(cache.v_scales + off[i]),
                                            (lptr_t)(sb + C::kVS + i * 256), 4, 0, 0);
@@ -279,7 +283,7 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
 #pragma unroll
               for (int w = 0; w < C::SW; ++w)
                 __builtin_amdgcn_global_load_lds(
-                    (gptr_t)(cache.k_scales + off[i] * (4 * C::SW) + w * 4),
+                    (gptr_t)(cache.k_scales + static_cast<int64_t>(off[i]) * (4 * C::SW) + w * 4),
                     (lptr_t)(sb + C::kKS + w * KT * 4 + to), 4, 0, 0);
               __builtin_amdgcn_global_load_lds((gptr_t)(cache.v_scales + off[i]),
                                                (lptr_t)(sb + C::kVS + to), 4, 0, 0);
@@ -291,11 +295,14 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
   };
 
   // The scores come out less the reference of their row (they start from its
-  // negative): 0 until the row sees a position, then kSlack above the largest score
-  // where it moved last, so that weights are 1 and less.  It moves when a score
-  // exceeds it.  seen: -inf before the row sees a position, 0 after.
+  // negative), which lies kSlack above the row's largest score where it moved last:
+  // 2^-kSlack is the largest weight then, and a lane's 32 add up to an eighth at most.
+  // It moves again when a lane's weights add up to more than 1, which takes no maximum
+  // over the scores in the other units.  most: that limit, or -1 until the row sees a
+  // position (its reference is 0 till then), so that any sum is over it.
+  constexpr float kMost = 1.0f;
   f32x4 o[OT];
-  float ref = 0.0f, seen = -INFINITY, l = 0.0f;
+  float ref = 0.0f, most = -1.0f, l = 0.0f;
 #pragma unroll
   for (int t = 0; t < OT; ++t) o[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
@@ -312,9 +319,9 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
   const int vkey = 64 * (n16 & 1) + 16 * (n16 >> 3) + 4 * g + ((n16 >> 1) & 3);
   const int voff = vkey * ROW + (swz_q4<D>(vkey) << 4);
 
-  // Unit u, the n-th of the item.
-  auto compute = [&](const char* sb, int u, int n) {
-    f32x4 st[8];
+  // The scores of unit u, less the references: st[t][r] of position 16 t + r and the
+  // lane's part 4 g.  dead, where masked: bit 4 t + r of positions that are not seen.
+  auto scores = [&](const char* sb, int u, int n, f32x4 (&st)[8], bool masked, uint32_t& dead) {
 #pragma unroll
     for (int hf = 0; hf < HALVES; ++hf) {
       u32x4 k[8];
@@ -325,74 +332,93 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
         ks[t] = static_cast<uint8_t>(sb[C::kKS + hf * KT * 4 + ksoff + t * 64]);
         if (C::kPad && (hf * 4 + kgroup) * 32 >= dim) ks[t] = 0;
       }
+      const f32x4 from = {-ref, -ref, -ref, -ref};
 #pragma unroll
-      for (int s = 0; s < QS; ++s)
+      for (int t = 0; t < 8; ++t) st[t] = mma_q4<0>(k[t], ks[t], qf[hf][0], qs[hf], hf ? st[t] : from);
 #pragma unroll
-        for (int t = 0; t < 8; ++t)
-          st[t] = mma_q4(k[t], ks[t], qf[hf][s], qs[hf][s],
-                         hf == 0 && s == 0 ? f32x4{-ref, -ref, -ref, -ref} : st[t]);
-    }
-    // Positions that are not seen, bit 4 t + r: 16 t + r and the lane's part 4 g.
-    const bool gone = missing[n & 3] == n + 1;
-    const bool masked = u * KT + KT - 1 > all_hi || u * KT < all_lo || gone;
-    uint32_t dead = 0;
-    if (masked) {
-      // a row that sees nothing has span 0 at a position that is none
-      const int d = u * KT + 4 * g - see_lo;
+      for (int t = 0; t < 8; ++t) st[t] = mma_q4<1>(k[t], ks[t], qf[hf][1], qs[hf], st[t]);
+      if constexpr (QS > 2) {
 #pragma unroll
-      for (int t = 0; t < 8; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          dead |= (static_cast<uint32_t>(d + t * 16 + r) > see_span ? 1u : 0u) << (4 * t + r);
-      if (gone) {
-        const int b0 = u * KT + lane;
-        const uint64_t page0 = __ballot(paged(table[fast_div(nearest(b0), a.bs)]));
-        const uint64_t page1 = __ballot(paged(table[fast_div(nearest(b0 + kWave), a.bs)]));
-#pragma unroll
-        for (int t = 0; t < 8; ++t)
-          dead |= (~static_cast<uint32_t>((t < 4 ? page0 : page1) >> (16 * (t & 3) + 4 * g)) & 15u)
-                  << (4 * t);
+        for (int t = 0; t < 8; ++t) st[t] = mma_q4<2>(k[t], ks[t], qf[hf][2], qs[hf], st[t]);
       }
+      if constexpr (QS > 3) {
 #pragma unroll
-      for (int t = 0; t < 8; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) st[t][r] = (dead >> (4 * t + r)) & 1 ? -INFINITY : st[t][r];
+        for (int t = 0; t < 8; ++t) st[t] = mma_q4<3>(k[t], ks[t], qf[hf][3], qs[hf], st[t]);
+      }
     }
-    float mx = st[0][0];
+    if (!masked) return;
+    // a row that sees nothing has span 0 at a position that is none
+    const int d = u * KT + 4 * g - see_lo;
+    dead = 0;
 #pragma unroll
     for (int t = 0; t < 8; ++t)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) mx = fmaxf(mx, st[t][r]);
-    mx = max_across<16>(mx);
-    mx = max_across<32>(mx);
-    if (__any(mx > seen)) {
-      const float up = mx > seen ? mx + kSlack : 0.0f;
-      const float f = __builtin_amdgcn_exp2f(seen - up);    // (nothing to keep before: 0)
-      seen = mx > seen ? 0.0f : seen;
+      for (int r = 0; r < 4; ++r)
+        dead |= (static_cast<uint32_t>(d + t * 16 + r) > see_span ? 1u : 0u) << (4 * t + r);
+    if (missing[n & 3] == n + 1) {
+      const int b0 = u * KT + lane;
+      const uint64_t page0 = __ballot(paged(table[fast_div(nearest(b0), a.bs)]));
+      const uint64_t page1 = __ballot(paged(table[fast_div(nearest(b0 + kWave), a.bs)]));
+#pragma unroll
+      for (int t = 0; t < 8; ++t)
+        dead |= (~static_cast<uint32_t>((t < 4 ? page0 : page1) >> (16 * (t & 3) + 4 * g)) & 15u)
+                << (4 * t);
+    }
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) st[t][r] = (dead >> (4 * t + r)) & 1 ? -INFINITY : st[t][r];
+  };
+  // The weights of the lane's positions and their sum; times their scales in x0 (the
+  // lower 64 positions) and x1 (the upper).
+  auto weigh = [&](const char* sb, const f32x4 (&st)[8], f32x16& x0, f32x16& x1) -> float {
+#pragma clang fp contract(off)
+    float sum = 0.0f;
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      const f32x4 vs = *reinterpret_cast<const f32x4*>(sb + C::kVS + (t * 16 + 4 * g) * 4);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float p = __builtin_amdgcn_exp2f(st[t][r]);
+        sum += p;
+        if (t < 4) x0[t * 4 + r] = p * vs[r];
+        else x1[(t - 4) * 4 + r] = p * vs[r];
+      }
+    }
+    return sum;
+  };
+  // Unit u, the n-th of the item.
+  auto compute = [&](const char* sb, int u, int n) {
+    const bool masked = u * KT + KT - 1 > all_hi || u * KT < all_lo || missing[n & 3] == n + 1;
+    uint32_t dead = 0;
+    f32x4 st[8];
+    f32x16 x0, x1;
+    scores(sb, u, n, st, masked, dead);
+    float sum = weigh(sb, st, x0, x1);
+    if (__any(sum > most)) {
+      asm volatile("" ::: "memory");        // (formed again: not held through the other units)
+      scores(sb, u, n, st, masked, dead);
+      float mx = st[0][0];
+#pragma unroll
+      for (int t = 0; t < 8; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) mx = fmaxf(mx, st[t][r]);
+      mx = max_across<16>(mx);
+      mx = max_across<32>(mx);
+      const bool first = most < 0.0f;           // the row has seen nothing before
+      const bool move = mx > (first ? -INFINITY : -kSlack);
+      const float up = move ? mx + kSlack : 0.0f;
+      const float f = move && first ? 0.0f : __builtin_amdgcn_exp2f(-up);
+      most = move ? kMost : most;
       ref += up;
       l *= f;
 #pragma unroll
       for (int t = 0; t < OT; ++t) o[t] *= f;
 #pragma unroll
       for (int t = 0; t < 8; ++t) st[t] -= up;
+      sum = weigh(sb, st, x0, x1);
     }
-    float sum = 0.0f;
-    f32x16 x0, x1;       // weights times scales: of the lower 64 positions, of the upper
-    uint32_t top = 0;
-    {
-#pragma clang fp contract(off)
-#pragma unroll
-      for (int t = 0; t < 8; ++t) {
-        const f32x4 vs = *reinterpret_cast<const f32x4*>(sb + C::kVS + (t * 16 + 4 * g) * 4);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float p = __builtin_amdgcn_exp2f(st[t][r]);
-          sum += p;
-          if (t < 4) x0[t * 4 + r] = p * vs[r];
-          else x1[(t - 4) * 4 + r] = p * vs[r];
-        }
-      }
-    }
+    asm volatile("" : "+v"(sum));       // formed here: 32 weights need not be held until later
     if (masked) {        // (their scales may be anything)
       const uint32_t gone_bits = fresh(static_cast<int>(dead));
 #pragma unroll
@@ -401,6 +427,7 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
         x1[i] = (gone_bits >> (16 + i)) & 1 ? 0.0f : x1[i];
       }
     }
+    uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < 16; ++i) top = max(max(top, __float_as_uint(x0[i])), __float_as_uint(x1[i]));
     l += sum;
@@ -475,7 +502,7 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
   if (row < it.rows && g == 0) {
     if (it.splits > 1) {
       const int64_t p = (static_cast<int64_t>(it.slot) * a.kv_heads + h) * C::MT + row;
-      a.part_ml[p * 2] = seen == 0.0f ? ref : -INFINITY;
+      a.part_ml[p * 2] = most < 0.0f ? -INFINITY : ref;
       a.part_ml[p * 2 + 1] = l;
     } else if (a.lse) {
       int token, head;
@@ -535,6 +562,7 @@ hipError_t launch_q4_rows(const AttendArgs& a, const Q4Cache& c, int mt, hipStre
     case 32: launch_q4_cfg<Q4Cfg<T, D, kPad, 2>>(a, c, st); break;
     case 48: launch_q4_cfg<Q4Cfg<T, D, kPad, 3>>(a, c, st); break;
     case 64: launch_q4_cfg<Q4Cfg<T, D, kPad, 4>>(a, c, st); break;
+    case 96: launch_q4_cfg<Q4Cfg<T, D, kPad, 6>>(a, c, st); break;
     case 128: launch_q4_cfg<Q4Cfg<T, D, kPad, 8>>(a, c, st); break;
     default: return hipErrorInvalidValue;
   }
