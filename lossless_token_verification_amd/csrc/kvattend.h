@@ -84,23 +84,47 @@ struct AttendPlanShared {
 // from cache, which costs less than the launch that a separate planning kernel
 // would be up to some 2000 sequences (single tokens over 1000 positions: 6.0 TB/s
 // of pages at 2048 of them, 5.2 at 4096).
-template <int MT, int KT, int WAVES>
+//
+// kHeld: the sequences of a thread that are read once and held in registers (each
+// pass reads them again where the batch has more, or with 0).
+template <int MT, int KT, int WAVES, int kHeld = 0>
 __device__ __forceinline__ bool attend_find(const AttendArgs& a, int x, bool count_slots,
                                             AttendPlanShared<WAVES>& sh, AttendItem& it) {
   constexpr int NT = WAVES * kWave;
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
   if (tid < kLengthClasses) sh.cls[tid] = 0;
   if (tid == 0) sh.found = 0;
+  AttendSeq held[kHeld > 0 ? kHeld : 1];
+  if constexpr (kHeld > 0) {
+    if (a.B > kHeld * NT) return attend_find<MT, KT, WAVES, 0>(a, x, count_slots, sh, it);
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      const int b = i * NT + tid;
+      held[i] = AttendSeq{};
+      if (b < a.B) held[i] = attend_seq<MT, KT>(a, b);
+    }
+  }
+  // f(b, sequence b) for this thread's sequences from the first-th on
+  auto each = [&](int first, auto f) {
+    if constexpr (kHeld > 0) {
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i)
+        if (i * NT + first < a.B) f(i * NT + first, held[i]);
+    } else {
+      for (int b = first; b < a.B; b += NT) f(b, attend_seq<MT, KT>(a, b));
+    }
+  };
   // Sums over the sequences, the same in every thread (the branches on them below
   // hold barriers): reduced, or, of one sequence, made by each thread for itself.
   uint64_t units = 0, tiles = 0;
   int longest = 0;
-  for (int b = a.B > 1 ? tid : 0; b < a.B; b += NT) {
-    const AttendSeq s = attend_seq<MT, KT>(a, b);
+  auto add = [&](int, const AttendSeq& s) {
     tiles += s.tiles;
     units += static_cast<uint64_t>(s.tiles) * s.units;
     if (s.tiles > 0) longest = max(longest, s.units);
-  }
+  };
+  if (a.B == 1) add(0, attend_seq<MT, KT>(a, 0));
+  else each(tid, add);
   if (a.B > 1) {
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) {
@@ -144,11 +168,10 @@ __device__ __forceinline__ bool attend_find(const AttendArgs& a, int x, bool cou
       items = tiles * max((static_cast<uint32_t>(longest) + S - 1) / S, 1u);
     } else if (tiles <= static_cast<uint64_t>(a.want_items)) {
       items = 0;
-      for (int b = tid; b < a.B; b += NT) {
-        const AttendSeq s = attend_seq<MT, KT>(a, b);
+      each(tid, [&](int, const AttendSeq& s) {
         items += static_cast<uint64_t>(s.tiles) *
                  max((static_cast<uint32_t>(s.units) + S - 1) / S, 1u);
-      }
+      });
 #pragma unroll
       for (int o = 32; o > 0; o >>= 1)
         items += __shfl_xor(static_cast<unsigned long long>(items), o, kWave);
@@ -175,12 +198,12 @@ __device__ __forceinline__ bool attend_find(const AttendArgs& a, int x, bool cou
   int my_cls = 0;
   uint64_t carry = 0, all = 0;   // (items << 32) + slots before this class, of the call
   if (a.B > 1) {
-    for (int b = tid; b < a.B; b += NT) {
+    each(tid, [&](int, const AttendSeq& s) {
       int splits, cls;
-      const uint64_t mine = shape(attend_seq<MT, KT>(a, b), splits, cls);
+      const uint64_t mine = shape(s, splits, cls);
       if (mine) atomicAdd(reinterpret_cast<unsigned long long*>(&sh.cls[cls]),
                           static_cast<unsigned long long>(mine));
-    }
+    });
     __syncthreads();
     const uint64_t n = lane < kLengthClasses ? sh.cls[lane] : 0;
     const uint64_t to = wave_prefix(n);
@@ -189,13 +212,13 @@ __device__ __forceinline__ bool attend_find(const AttendArgs& a, int x, bool cou
     my_cls = with ? __builtin_ctzll(with) : -1;
     carry = with ? __shfl(static_cast<unsigned long long>(to - n), my_cls, kWave) : 0;
   }
-  for (int c = 0; c < a.B && my_cls >= 0; c += NT) {
+  bool done = my_cls < 0;
+  // sequences c .. c + NT - 1, one a thread; all threads agree on `done`
+  auto search = [&](int c, const AttendSeq& s) {
     const int b = c + tid;
-    AttendSeq s{};
     int splits = 1;
     uint64_t mine = 0;
     if (b < a.B) {
-      s = attend_seq<MT, KT>(a, b);
       int cls;
       mine = shape(s, splits, cls);
       if (a.B == 1) all = mine;
@@ -247,7 +270,18 @@ __device__ __forceinline__ bool attend_find(const AttendArgs& a, int x, bool cou
       sh.item = r;
       sh.found = 1;
     }
-    if (static_cast<int64_t>(carry >> 32) > x) break;
+    done = static_cast<int64_t>(carry >> 32) > x;
+  };
+  if constexpr (kHeld > 0) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (i * NT < a.B && !done) search(i * NT, held[i]);
+  } else {
+    for (int c = 0; c < a.B && !done; c += NT) {
+      AttendSeq s{};
+      if (c + tid < a.B) s = attend_seq<MT, KT>(a, c + tid);
+      search(c, s);
+    }
   }
   if (count_slots && tid == 0)   // (thread 0 has the one sequence where B = 1)
     *a.slot_count = static_cast<int32_t>(min(static_cast<uint32_t>(all),

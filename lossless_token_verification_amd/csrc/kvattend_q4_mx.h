@@ -46,12 +46,28 @@ __device__ __forceinline__ f32x4 mma_q4(u32x4 codes, int code_scale, u32x6 piece
                                                           piece_scale);
 }
 
+// 32 numbers, even ones in x0 and odd ones in x1, over the power of two s as 6-bit
+// numbers (ties to even, at most 7.5), and back.  The instructions write their results
+// while they still read, so the two may share no register: the early clobber says so
+// (the compiler's own forms of them do not, and it does let them overlap).  A matrix
+// instruction may read the result two states later; the compiler, which does not see
+// what is in here, would not wait for that.
+__device__ __forceinline__ u32x6 to_fp6(f32x16 x0, f32x16 x1, float s) {
+  u32x6 y;
+  asm("v_cvt_scalef32_2xpk16_fp6_f32 %0, %1, %2, %3\n\ts_nop 1"
+      : "=&v"(y) : "v"(x0), "v"(x1), "v"(s));
+  return y;
+}
+__device__ __forceinline__ f32x32 from_fp6(u32x6 x, float s) {
+  f32x32 y;
+  asm("v_cvt_scalef32_pk32_f32_fp6 %0, %1, %2" : "=&v"(y) : "v"(x), "v"(s));
+  return y;
+}
+
 // The N pieces of 32 numbers, even ones in x0 and odd ones in x1, the largest of
 // magnitude `top` (as bits).  add: what the scales' exponents are raised by.  Two
 // pieces are scaled so that the largest is in (3.75, 7.5], more so that it is in [2, 4).
-// The conversions read their sources while they write, so their sources have to
-// outlive them: the empty statements keep the registers apart.  Numbers below 2^-104
-// lose bits (the last piece's scale is 2^-118 at least).
+// Numbers below 2^-104 lose bits (the last piece's scale is 2^-118 at least).
 template <int N>
 __device__ __forceinline__ void split_pieces(f32x16 x0, f32x16 x1, uint32_t top, int add,
                                              u32x6 (&piece)[N], int (&scale)[N]) {
@@ -61,13 +77,11 @@ __device__ __forceinline__ void split_pieces(f32x16 x0, f32x16 x1, uint32_t top,
 #pragma unroll
   for (int p = 0; p < N; ++p) {
     const float s = __uint_as_float(static_cast<uint32_t>(min(b, 254) - 5 * p) << 23);
-    piece[p] = __builtin_amdgcn_cvt_scalef32_2xpk16_fp6_f32(x0, x1, s);
-    asm volatile("" : "+v"(piece[p]) : "v"(x0), "v"(x1), "v"(s));
+    piece[p] = to_fp6(x0, x1, s);
     // infinity or NaN among them: NaN
     scale[p] = top >= 0x7f800000u || b + add > 254 ? 255 : max(b + add - 5 * p, 0);
     if (p + 1 < N) {
-      f32x32 y = __builtin_amdgcn_cvt_scalef32_pk32_f32_fp6(piece[p], s);
-      asm volatile("" : "+v"(y) : "v"(piece[p]), "v"(s));
+      const f32x32 y = from_fp6(piece[p], s);
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         x0[i] -= y[2 * i];
@@ -105,7 +119,8 @@ struct Q4Cfg {
   static constexpr int CHUNKS = (LOADS + W - 1) / W;       // loads of a wavefront
   static constexpr int IDS = (CHUNKS * RPL + kWave - 1) / kWave;   // its lookups, per unit
   static constexpr int OT = D / 16;                        // result tiles
-  static constexpr bool kOnce = MT <= 64;                  // as in the 16-bit kernel
+  static constexpr int kHeld = W < 3 ? 4 : 2;              // sequences that a thread plans for
+  static constexpr bool kOnce = MT <= 48;                  // nontemporal: one tile a sequence
   static constexpr int kPerSimd = D == 256 || W == 1 || (D == 128 && W == 2) ? 2 : 3;   // wavefronts
 };
 
@@ -125,15 +140,20 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
   constexpr int IDS = C::IDS, CHUNKS = C::CHUNKS, HALVES = C::HALVES, QS = C::QS, PQ = C::PQ, PP = C::PP;
   // (two LDS objects: a direct load into one is known to leave the other alone)
   __shared__ __attribute__((aligned(1024))) char sb0[C::BYTES], sb1[C::BYTES];
-  __shared__ __attribute__((aligned(256))) int32_t sid[C::W * IDS * kWave];
-  __shared__ int32_t missing[4];   // unit + 1 where a page of the unit is missing
+  __shared__ __attribute__((aligned(256))) int32_t sid[C::W * 2 * IDS * kWave];
+  __shared__ int32_t missing[8];   // unit + 1 where a page of the unit is missing
   __shared__ AttendPlanShared<C::W> plan;
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int dim = C::kPad ? a.D : D, row_bytes = dim / 2;
-  const int x = blockIdx.x / a.kv_heads, h = blockIdx.x - x * a.kv_heads;
+  int x = blockIdx.x / a.kv_heads, h = blockIdx.x - x * a.kv_heads;
+  if (C::kOnce) {
+    const int r = blockIdx.x >> 3, q = r / a.kv_heads;
+    h = r - q * a.kv_heads;
+    x = q * 8 + (blockIdx.x & 7);
+  }
   AttendItem it;
-  if (!attend_find<C::MT, KT, C::W>(a, x, a.max_slots > 0 && blockIdx.x == 0, plan, it)) return;
+  if (!attend_find<C::MT, KT, C::W, C::kHeld>(a, x, a.max_slots > 0 && blockIdx.x == 0, plan, it)) return;
   if (it.splits > 1 && h == 0 && tid == 0) attend_slot_info(a, it);
 
   // this lane's query row (rows past the tile repeat its last one) and the quarter
@@ -142,32 +162,151 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
   const int row = wave * 16 + (lane & 15);
   int see_lo;
   uint32_t see_span;     // the positions it sees: see_span of them from see_lo on, and that one
-  u32x6 qf[HALVES][QS];
-  int qs[HALVES];        // a byte for each step's pieces
+  int q_token, q_head;
   {
-    int token, head;
-    attend_row(a, it.token0, it.row0 + min(row, it.rows - 1), h, token, head);
-    const int pos = it.pos0 + token - it.token0;
+    attend_row(a, it.token0, it.row0 + min(row, it.rows - 1), h, q_token, q_head);
+    const int pos = it.pos0 + q_token - it.token0;
     const int key_last = min(pos, it.key_hi - 1);
     const int key_first = a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
     see_lo = key_last >= key_first ? key_first : INT32_MAX;
     see_span = key_last >= key_first ? key_last - key_first : 0;
+  }
+  // positions every row of the tile may see: units inside need no mask
+  const int all_hi = min(it.pos0 + fast_div(it.row0, a.grp), it.key_hi - 1);
+  const int pos_last = it.pos0 + fast_div(it.row0 + it.rows - 1, a.grp);
+  const int all_lo = a.window > 0 && pos_last >= a.window ? pos_last - a.window + 1 : 0;
+
+  const int32_t* table = a.table + static_cast<int64_t>(it.b) * a.max_blocks;
+  // (rows of the cache are numbered in 32 bits)
+  const uint32_t head_rows = static_cast<uint32_t>(h) * a.block_size;
+  const uint32_t block_rows = static_cast<uint32_t>(a.kv_heads) * a.block_size;
+  // A unit's rows are loaded RPL at a time, CHUNKS loads of neighbouring rows by each
+  // wavefront.  Lane l looks up the l-th of its wavefront's rows (and the 64 + l-th): its
+  // number in the cache, and whether there is such a page.  Positions outside the
+  // item's range read the nearest one inside (and are masked); a missing page reads
+  // block 0.
+  const int wave_row = wave * (CHUNKS * RPL);
+  auto in_unit = [&](int i) { return wave_row + i * kWave + lane; };   // (may be past the unit)
+  auto own_row = [&](int i) { return i * kWave + lane < CHUNKS * RPL && in_unit(i) < KT; };
+  auto nearest = [&](int key) { return min(max(key, it.key_lo), it.key_hi - 1); };
+  auto paged = [&](int id) { return id >= 0 && id < a.num_blocks; };
+  int32_t* const ids = sid + wave * (2 * IDS * kWave);
+  auto look = [&](int slot, int base) {     // starts the lookups of the unit at position `base`
+#pragma unroll
+    for (int i = 0; i < IDS; ++i)
+      __builtin_amdgcn_global_load_lds((gptr_t)(table + fast_div(nearest(base + in_unit(i)), a.bs)),
+                                       (lptr_t)(ids + (slot * IDS + i) * kWave), 4, 0, 0);
+  };
+  uint32_t off[IDS];
+  auto turn = [&](int slot, int n, int base) {   // the n-th unit, looked up, is the next to load
+#pragma unroll
+    for (int i = 0; i < IDS; ++i) {
+      const int id = ids[(slot * IDS + i) * kWave + lane];
+      const int key = nearest(base + in_unit(i));
+      off[i] = (paged(id) ? id : 0) * block_rows + head_rows +
+               (key - fast_div(key, a.bs) * a.block_size);
+      if (__any(!paged(id) && own_row(i))) missing[n & 7] = n + 1;
+    }
+  };
+  // Loads the unit at position `base` into LDS.  Inside the item's range, with whole
+  // pages of rows, a load's address is one lane's row plus a lane constant and moves
+  // through scalar registers.
+  const int lq = lane / NV, lslot = lane & (NV - 1);
+  const bool whole_rows = a.block_size % RPL == 0;
+  auto load_unit = [&](int base, char* sb) {
+    const bool inside = whole_rows && base >= it.key_lo && base + KT <= it.key_hi;
+#pragma unroll
+    for (int i = 0; i < CHUNKS; ++i) {
+      const int j = wave * CHUNKS + i;               // which RPL rows
+      if (C::LOADS % CHUNKS != 0 || C::W * CHUNKS > C::LOADS)
+        if (j >= C::LOADS) break;
+      const int from = i * RPL & (kWave - 1);
+      const uint32_t rows = off[i * RPL / kWave];
+      const int vec = lslot ^ swz_q4<D>(j * RPL + lq);
+      if (inside) {
+        const uint32_t r = __builtin_amdgcn_readlane(rows, from);
+        const int64_t at = static_cast<int64_t>(r) * row_bytes;
+        const uint32_t in = fresh(lq * row_bytes + vec * 16);
+        if (!C::kPad || vec * 16 < row_bytes) {
+          load_lds<C::kOnce>(cache.k_codes + at + in, sb + j * 1024);
+          load_lds<C::kOnce>(cache.v_codes + at + in, sb + C::kV + j * 1024);
+        }
+        asm volatile("; scalar addresses");   // keeps the two forms from being merged
+      } else {
+        const uint32_t r = __shfl(rows, from + lq, kWave);
+        const int64_t at = static_cast<int64_t>(r) * row_bytes + fresh(vec * 16);
+        if (!C::kPad || vec * 16 < row_bytes) {
+          load_lds<C::kOnce>(cache.k_codes + at, sb + j * 1024);
+          load_lds<C::kOnce>(cache.v_codes + at, sb + C::kV + j * 1024);
+        }
+      }
+    }
+    // the scales of the same rows (a direct load's place in LDS is one for the
+    // wavefront, and 4 bytes on for each lane: neighbouring rows need one load)
+#pragma unroll
+    for (int i = 0; i < IDS; ++i) {
+      if (!own_row(i)) continue;
+      const int to = (wave_row + i * kWave) * 4;
+#pragma unroll
+      for (int w = 0; w < C::SW; ++w)
+        __builtin_amdgcn_global_load_lds(
+            (gptr_t)(cache.k_scales + static_cast<int64_t>(off[i]) * (4 * C::SW) + w * 4),
+            (lptr_t)(sb + C::kKS + w * KT * 4 + to), 4, 0, 0);
+      __builtin_amdgcn_global_load_lds((gptr_t)(cache.v_scales + off[i]),
+                                       (lptr_t)(sb + C::kVS + to), 4, 0, 0);
+    }
+  };
+
+  // The queries, the first lookups and loads.
+  u32x4 raw[HALVES][4];
+  {
+    const T* qr = static_cast<const T*>(a.q) + q_token * a.q_stride + static_cast<int64_t>(q_head) * dim;
+#pragma unroll
+    for (int hf = 0; hf < HALVES; ++hf) {
+      const int group = D == 64 ? g & 1 : hf * 4 + g;      // the lane's 32 channels
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        raw[hf][i] = u32x4{0, 0, 0, 0};
+        if (!C::kPad || group * 32 < dim) raw[hf][i] = reinterpret_cast<const u32x4*>(qr)[group * 4 + i];
+      }
+    }
+  }
+  const int n_units = it.u1 - it.u0;
+  const int first = it.u0 * KT;
+  if (n_units > 0) {
+    look(0, first);
+    look(1, first + KT);
+    if (C::kPad) {
+      // (vectors that a row does not have are loaded by no one: zero from here on)
+      for (int i = tid; i < C::kKS / 16; i += C::W * kWave) {
+        reinterpret_cast<u32x4*>(sb0)[i] = u32x4{0, 0, 0, 0};
+        reinterpret_cast<u32x4*>(sb1)[i] = u32x4{0, 0, 0, 0};
+      }
+    }
+    if (tid < 8) missing[tid] = 0;
+    wait_loads();
+    __syncthreads();
+    turn(0, 0, first);
+    load_unit(first, sb0);
+    turn(1, 1, first + KT);
+    wait_entries();
+    look(0, first + 2 * KT);
+  }
+  u32x6 qf[HALVES][QS];
+  int qs[HALVES];        // a byte for each step's pieces
+  {
     // scores in log2 units: the factor's significand goes into the queries, its
     // exponent into their scales
     int factor_exp;
     const float factor = frexpf(a.scale * kLog2e, &factor_exp);
-    const T* qr = static_cast<const T*>(a.q) + token * a.q_stride + static_cast<int64_t>(head) * dim;
 #pragma unroll
     for (int hf = 0; hf < HALVES; ++hf) {
-      const int group = D == 64 ? g & 1 : hf * 4 + g;      // its 32 channels
       f32x16 x0, x1;
       uint32_t top = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        u32x4 w = {0, 0, 0, 0};
-        if (!C::kPad || group * 32 < dim) w = reinterpret_cast<const u32x4*>(qr)[group * 4 + i];
         typedef T t8 __attribute__((ext_vector_type(8)));
-        const t8 v = __builtin_bit_cast(t8, w);
+        const t8 v = __builtin_bit_cast(t8, raw[hf][i]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           x0[i * 4 + j] = static_cast<float>(v[2 * j]) * factor;
@@ -192,108 +331,6 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
       }
     }
   }
-  // positions every row of the tile may see: units inside need no mask
-  const int all_hi = min(it.pos0 + fast_div(it.row0, a.grp), it.key_hi - 1);
-  const int pos_last = it.pos0 + fast_div(it.row0 + it.rows - 1, a.grp);
-  const int all_lo = a.window > 0 && pos_last >= a.window ? pos_last - a.window + 1 : 0;
-
-  const int32_t* table = a.table + static_cast<int64_t>(it.b) * a.max_blocks;
-  // (rows of the cache are numbered in 32 bits)
-  const uint32_t head_rows = static_cast<uint32_t>(h) * a.block_size;
-  const uint32_t block_rows = static_cast<uint32_t>(a.kv_heads) * a.block_size;
-  // A unit's rows are loaded RPL at a time, load j by wavefront j % W.  Lane l looks up
-  // the l-th row of its wavefront's loads (and the 64 + l-th): its row number in the
-  // cache, and whether there is such a page.  Positions outside the item's range read
-  // the nearest one inside (and are masked); a missing page reads block 0.
-  auto in_unit = [&](int i) {       // position in the unit of the wavefront's row i * 64 + lane
-    const int r = i * kWave + lane;
-    return ((r / RPL) * C::W + wave) * RPL + r % RPL;
-  };
-  auto nearest = [&](int key) { return min(max(key, it.key_lo), it.key_hi - 1); };
-  auto paged = [&](int id) { return id >= 0 && id < a.num_blocks; };
-  int32_t* const ids = sid + wave * (IDS * kWave);
-  auto look = [&](int base) {       // starts the lookups of the unit at position `base`
-#pragma unroll
-    for (int i = 0; i < IDS; ++i)
-      __builtin_amdgcn_global_load_lds((gptr_t)(table + fast_div(nearest(base + in_unit(i)), a.bs)),
-                                       (lptr_t)(ids + i * kWave), 4, 0, 0);
-  };
-  uint32_t off[IDS];
-  auto turn = [&](int n, int base) {    // the unit looked up (the n-th) becomes the next to load
-#pragma unroll
-    for (int i = 0; i < IDS; ++i) {
-      const int id = ids[i * kWave + lane];
-      const int key = nearest(base + in_unit(i));
-      off[i] = (paged(id) ? id : 0) * block_rows + head_rows +
-               (key - fast_div(key, a.bs) * a.block_size);
-      if (__any(!paged(id) && in_unit(i) < KT)) missing[n & 3] = n + 1;
-    }
-  };
-  // Loads the unit at position `base` into LDS.  Inside the item's range, with whole
-  // pages of rows, a load's address is one lane's row plus a lane constant and moves
-  // through scalar registers.
-  const int lq = lane / NV, lslot = lane & (NV - 1);
-  const bool whole_rows = a.block_size % RPL == 0;
-  auto load_unit = [&](int base, char* sb) {
-    const bool inside = whole_rows && base >= it.key_lo && base + KT <= it.key_hi;
-#pragma unroll
-    for (int i = 0; i < CHUNKS; ++i) {
-      const int j = wave + i * C::W;                 // which RPL rows
-      if (C::LOADS % C::W != 0 && j >= C::LOADS) break;
-      const int from = i * RPL & (kWave - 1);
-      const uint32_t mine = off[i * RPL / kWave];
-      const int vec = lslot ^ swz_q4<D>(j * RPL + lq);
-      if (inside) {
-        const int64_t at = static_cast<int64_t>(__builtin_amdgcn_readlane(mine, from)) * row_bytes;
-        const uint32_t in = fresh(lq * row_bytes + vec * 16);
-        if (!C::kPad || vec * 16 < row_bytes) {
-          load_lds<C::kOnce>(cache.k_codes + at + in, sb + j * 1024);
-          load_lds<C::kOnce>(cache.v_codes + at + in, sb + C::kV + j * 1024);
-        }
-        asm volatile("; scalar addresses");   // keeps the two forms from being merged
-      } else {
-        const uint32_t r = __shfl(mine, from + lq, kWave);
-        const int64_t at = static_cast<int64_t>(r) * row_bytes + fresh(vec * 16);
-        if (!C::kPad || vec * 16 < row_bytes) {
-          load_lds<C::kOnce>(cache.k_codes + at, sb + j * 1024);
-          load_lds<C::kOnce>(cache.v_codes + at, sb + C::kV + j * 1024);
-        }
-      }
-    }
-    // the scales of the same rows, a run of RPL lanes for each load
-    if (C::W <= C::LOADS || wave < C::LOADS) {
-#pragma unroll
-      for (int i = 0; i < IDS; ++i) {
-        if constexpr (C::W == 1) {          // rows in order: 64 at a time
-#pragma unroll
-          for (int w = 0; w < C::SW; ++w)
-            __builtin_amdgcn_global_load_lds((gptr_t)(cache.k_scales + static_cast<int64_t>(off[i]) * (4 * C::SW) + w * 4),
-                                             (lptr_t)(sb + C::kKS + w * KT * 4 + i * 256), 4, 0, 0);
-          __builtin_amdgcn_global_load_lds((gptr_t)(cache.v_scales + off[i]),
-                                           (lptr_t)(sb + C::kVS + i * 256), 4, 0, 0);
-        } else {
-          // (lane l of a load writes to its base + 4 l: the base that puts lane
-          // c RPL at row j RPL)
-#pragma unroll
-          for (int c = 0; c < kWave / RPL && i * (kWave / RPL) + c < CHUNKS; ++c) {
-            const int j = wave + (i * (kWave / RPL) + c) * C::W;
-            if (C::LOADS % C::W != 0 && j >= C::LOADS) break;
-            const int to = (j - c) * RPL * 4;
-            if (lane / RPL == c) {
-#pragma unroll
-              for (int w = 0; w < C::SW; ++w)
-                __builtin_amdgcn_global_load_lds(
-                    (gptr_t)(cache.k_scales + static_cast<int64_t>(off[i]) * (4 * C::SW) + w * 4),
-                    (lptr_t)(sb + C::kKS + w * KT * 4 + to), 4, 0, 0);
-              __builtin_amdgcn_global_load_lds((gptr_t)(cache.v_scales + off[i]),
-                                               (lptr_t)(sb + C::kVS + to), 4, 0, 0);
-            }
-          }
-        }
-      }
-    }
-  };
-
   // The scores come out less the reference of their row (they start from its
   // negative), which lies kSlack above the row's largest score where it moved last:
   // 2^-kSlack is the largest weight then, and a lane's 32 add up to an eighth at most.
@@ -355,7 +392,7 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
 #pragma unroll
       for (int r = 0; r < 4; ++r)
         dead |= (static_cast<uint32_t>(d + t * 16 + r) > see_span ? 1u : 0u) << (4 * t + r);
-    if (missing[n & 3] == n + 1) {
+    if (missing[n & 7] == n + 1) {
       const int b0 = u * KT + lane;
       const uint64_t page0 = __ballot(paged(table[fast_div(nearest(b0), a.bs)]));
       const uint64_t page1 = __ballot(paged(table[fast_div(nearest(b0 + kWave), a.bs)]));
@@ -389,7 +426,7 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
   };
   // Unit u, the n-th of the item.
   auto compute = [&](const char* sb, int u, int n) {
-    const bool masked = u * KT + KT - 1 > all_hi || u * KT < all_lo || missing[n & 3] == n + 1;
+    const bool masked = u * KT + KT - 1 > all_hi || u * KT < all_lo || missing[n & 7] == n + 1;
     uint32_t dead = 0;
     f32x4 st[8];
     f32x16 x0, x1;
@@ -454,44 +491,22 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
     }
   };
 
-  const int n_units = it.u1 - it.u0;
   if (n_units > 0) {
     // Step n computes unit n from buffer n % 2 while unit n + 1 is under way; the
     // table entries of unit n + 2 are turned into addresses meanwhile and those of
     // unit n + 3 looked up, into LDS as well.  Loads past the last unit read its
     // nearest position again.
-    if (C::kPad) {
-      // (vectors that a row does not have are loaded by no one: zero from here on)
-      for (int i = tid; i < C::kKS / 16; i += C::W * kWave) {
-        reinterpret_cast<u32x4*>(sb0)[i] = u32x4{0, 0, 0, 0};
-        reinterpret_cast<u32x4*>(sb1)[i] = u32x4{0, 0, 0, 0};
-      }
-    }
-    if (tid < 4) missing[tid] = 0;
-    const int first = it.u0 * KT;
-    look(first);
-    wait_loads();
-    __syncthreads();
-    turn(0, first);
-    wait_loads();                     // the entries are read before the next overwrite them
-    load_unit(first, sb0);
-    look(first + KT);
-    wait_loads();
-    turn(1, first + KT);
-    wait_loads();
-    look(first + 2 * KT);
-    auto step = [&](int n, char* now, char* next) {
+    auto step = [&](int n, int slot, char* now, char* next) {
       wait_loads();
       __builtin_amdgcn_s_barrier();
       load_unit(first + (n + 1) * KT, next);
-      turn(n + 2, first + (n + 2) * KT);
-      wait_entries();
-      look(first + (n + 3) * KT);
+      turn(slot, n + 2, first + (n + 2) * KT);
+      look(1 - slot, first + (n + 3) * KT);
       if (n < n_units) compute(now, it.u0 + n, n);
     };
     for (int n = 0; n < n_units; n += 2) {
-      step(n, sb0, sb1);
-      step(n + 1, sb1, sb0);
+      step(n, 0, sb0, sb1);
+      step(n + 1, 1, sb1, sb0);
     }
     // no load may still be under way when the workgroup gives its LDS back
     wait_loads();
@@ -551,7 +566,8 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
 
 template <class C>
 void launch_q4_cfg(const AttendArgs& a, const Q4Cache& c, hipStream_t st) {
-  hipLaunchKernelGGL(attend_q4_kernel<C>, dim3(static_cast<unsigned>(a.grid_items) * a.kv_heads),
+  const unsigned items = C::kOnce ? (static_cast<unsigned>(a.grid_items) + 7) / 8 * 8 : a.grid_items;
+  hipLaunchKernelGGL(attend_q4_kernel<C>, dim3(items * a.kv_heads),
                      dim3(C::W * kWave), 0, st, a, c);
 }
 
@@ -562,8 +578,6 @@ hipError_t launch_q4_rows(const AttendArgs& a, const Q4Cache& c, int mt, hipStre
     case 32: launch_q4_cfg<Q4Cfg<T, D, kPad, 2>>(a, c, st); break;
     case 48: launch_q4_cfg<Q4Cfg<T, D, kPad, 3>>(a, c, st); break;
     case 64: launch_q4_cfg<Q4Cfg<T, D, kPad, 4>>(a, c, st); break;
-    case 96: launch_q4_cfg<Q4Cfg<T, D, kPad, 6>>(a, c, st); break;
-    case 128: launch_q4_cfg<Q4Cfg<T, D, kPad, 8>>(a, c, st); break;
     default: return hipErrorInvalidValue;
   }
   return hipGetLastError();
