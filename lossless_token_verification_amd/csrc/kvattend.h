@@ -33,12 +33,13 @@ __device__ __forceinline__ AttendSeq attend_seq(const AttendArgs& a, int b) {
   const int L = max(a.lens[b], 0);
   s.token0 = c0;
   s.n = c1 - c0;
-  s.pos0 = static_cast<int64_t>(L) - s.n;
+  // (32 bits hold all of it: n * group <= T * heads < 2^31, and L - n >= -2^31 + 1)
+  const int pos0 = L - s.n;
+  s.pos0 = pos0;
   s.kmax = min(L, a.cap);
-  s.tiles = static_cast<int>((static_cast<int64_t>(s.n) * a.group + MT - 1) / MT);
-  const int64_t lo = a.window > 0 ? max(s.pos0 - a.window + 1, static_cast<int64_t>(0)) : 0;
-  s.units = s.kmax > lo ? static_cast<int>((s.kmax + static_cast<int64_t>(KT) - 1) / KT - lo / KT)
-                        : 0;
+  s.tiles = static_cast<int>((static_cast<uint32_t>(s.n) * static_cast<uint32_t>(a.group) + MT - 1) / MT);
+  const int lo = a.window > 0 && pos0 >= a.window ? pos0 - a.window + 1 : 0;
+  s.units = s.kmax > lo ? static_cast<int>((static_cast<uint32_t>(s.kmax) + KT - 1) / KT) - lo / KT : 0;
   return s;
 }
 
@@ -189,8 +190,10 @@ __device__ __forceinline__ bool attend_find(const AttendArgs& a, int x, bool cou
   const int top = min(longest, S);
   auto shape = [&](const AttendSeq& s, int& splits, int& cls) -> uint64_t {
     splits = s.units > S ? static_cast<int>((static_cast<uint32_t>(s.units) + S - 1) / S) : 1;
-    const float len = static_cast<float>(s.units) / static_cast<float>(splits);
-    const int c = static_cast<int>(len * kLengthClasses / static_cast<float>(top + 1));
+    // (any class is right: it only orders the items, the same way in every workgroup)
+    const float len = static_cast<float>(s.units) * kLengthClasses /
+                      (static_cast<float>(splits) * static_cast<float>(top + 1));
+    const int c = static_cast<int>(len);
     cls = kLengthClasses - 1 - min(max(c, 0), kLengthClasses - 1);
     const uint64_t items = static_cast<uint64_t>(s.tiles) * splits;
     return (items << 32) + (splits > 1 ? items : 0);
