@@ -357,8 +357,10 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
   const int voff = vkey * ROW + (swz_q4<D>(vkey) << 4);
 
   // The scores of unit u, less the references: st[t][r] of position 16 t + r and the
-  // lane's part 4 g.  dead, where masked: bit 4 t + r of positions that are not seen.
-  auto scores = [&](const char* sb, int u, int n, f32x4 (&st)[8], bool masked, uint32_t& dead) {
+  // lane's part 4 g, -inf where it is not seen (masked: there may be such; dead: their
+  // bits 4 t + r).
+  auto scores = [&](const char* sb, int u, int n, f32x4 (&st)[8], bool masked,
+                    uint32_t& dead) {
 #pragma unroll
     for (int hf = 0; hf < HALVES; ++hf) {
       u32x4 k[8];
@@ -424,44 +426,49 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
     }
     return sum;
   };
-  // Unit u, the n-th of the item.
-  auto compute = [&](const char* sb, int u, int n) {
+  // Moves the references to these scores (less the old ones).
+  auto move_up = [&](f32x4 (&st)[8]) {
+    float mx = st[0][0];
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) mx = fmaxf(mx, st[t][r]);
+    mx = max_across<16>(mx);
+    mx = max_across<32>(mx);
+    const bool first = most < 0.0f;           // the row has seen nothing before
+    const bool move = mx > (first ? -INFINITY : -kSlack);
+    const float up = move ? mx + kSlack : 0.0f;
+    const float f = move && first ? 0.0f : __builtin_amdgcn_exp2f(-up);
+    most = move ? kMost : most;
+    ref += up;
+    l *= f;
+#pragma unroll
+    for (int t = 0; t < OT; ++t) o[t] *= f;
+#pragma unroll
+    for (int t = 0; t < 8; ++t) st[t] -= up;
+  };
+  // Unit u, the n-th of the item; kFirst: n is 0.
+  auto compute = [&](auto kFirst, const char* sb, int u, int n) {
     const bool masked = u * KT + KT - 1 > all_hi || u * KT < all_lo || missing[n & 7] == n + 1;
     uint32_t dead = 0;
     f32x4 st[8];
     f32x16 x0, x1;
     scores(sb, u, n, st, masked, dead);
+    if (decltype(kFirst)::value) move_up(st);
     float sum = weigh(sb, st, x0, x1);
-    if (__any(sum > most)) {
+    if (!decltype(kFirst)::value && __any(sum > most)) {
       asm volatile("" ::: "memory");        // (formed again: not held through the other units)
       scores(sb, u, n, st, masked, dead);
-      float mx = st[0][0];
-#pragma unroll
-      for (int t = 0; t < 8; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) mx = fmaxf(mx, st[t][r]);
-      mx = max_across<16>(mx);
-      mx = max_across<32>(mx);
-      const bool first = most < 0.0f;           // the row has seen nothing before
-      const bool move = mx > (first ? -INFINITY : -kSlack);
-      const float up = move ? mx + kSlack : 0.0f;
-      const float f = move && first ? 0.0f : __builtin_amdgcn_exp2f(-up);
-      most = move ? kMost : most;
-      ref += up;
-      l *= f;
-#pragma unroll
-      for (int t = 0; t < OT; ++t) o[t] *= f;
-#pragma unroll
-      for (int t = 0; t < 8; ++t) st[t] -= up;
+      move_up(st);
       sum = weigh(sb, st, x0, x1);
     }
     asm volatile("" : "+v"(sum));       // formed here: 32 weights need not be held until later
     if (masked) {        // (their scales may be anything)
-      const uint32_t gone_bits = fresh(static_cast<int>(dead));
+      const uint32_t gone = fresh(static_cast<int>(dead));
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        x0[i] = (gone_bits >> i) & 1 ? 0.0f : x0[i];
-        x1[i] = (gone_bits >> (16 + i)) & 1 ? 0.0f : x1[i];
+        x0[i] = (gone >> i) & 1 ? 0.0f : x0[i];
+        x1[i] = (gone >> (16 + i)) & 1 ? 0.0f : x1[i];
       }
     }
     uint32_t top = 0;
@@ -496,17 +503,18 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
     // table entries of unit n + 2 are turned into addresses meanwhile and those of
     // unit n + 3 looked up, into LDS as well.  Loads past the last unit read its
     // nearest position again.
-    auto step = [&](int n, int slot, char* now, char* next) {
+    auto step = [&](auto kFirst, int n, int slot, char* now, char* next) {
       wait_loads();
       __builtin_amdgcn_s_barrier();
       load_unit(first + (n + 1) * KT, next);
       turn(slot, n + 2, first + (n + 2) * KT);
       look(1 - slot, first + (n + 3) * KT);
-      if (n < n_units) compute(now, it.u0 + n, n);
+      if (n < n_units) compute(kFirst, now, it.u0 + n, n);
     };
-    for (int n = 0; n < n_units; n += 2) {
-      step(n, 0, sb0, sb1);
-      step(n + 1, 1, sb1, sb0);
+    step(std::true_type{}, 0, 0, sb0, sb1);
+    for (int n = 1; n < n_units; n += 2) {
+      step(std::false_type{}, n, 1, sb1, sb0);
+      step(std::false_type{}, n + 1, 0, sb0, sb1);
     }
     // no load may still be under way when the workgroup gives its LDS back
     wait_loads();
