@@ -284,13 +284,15 @@ size_t kv_paged_attention_q4_workspace_bytes(const spec_kv_attention_desc* desc)
 
 /* kv_paged_attention over a 4-bit cache: q and out bfloat16 or float16 (desc.dtype),
  * head_dim a multiple of 32, desc.block_stride 0, everything else as there.
- * Products on the matrix cores, on the codes as they lie: a query is split into
- * pieces of 4 significant bits, relative to the largest of 32 channels, whose sum is off
- * by 2^-14 of that at most (bf16; 2^-19 in f16), a softmax weight times its
- * value's scale into pieces relative to the largest of 32 positions, off by 2^-9 of
- * that at most (bf16; 2^-14 in f16).  Sums are float32.  A query row with an
- * infinity or NaN gets NaN in out and lse if it sees a position.  Values at
- * positions a row does not see never reach it, whatever their scales hold. */
+ * num_blocks * block_size * kv_heads < 2^32.
+ * Products on the matrix cores, on the codes as they lie, float32 sums.  What stands
+ * against the codes is split into pieces of 4 significant bits with a power of two
+ * per 32.  A query's pieces add up to it within 2^-14 of the largest of 32 channels
+ * (bf16; 2^-19 in f16).  A softmax weight times its value's scale, x: within 2^-8 |x| +
+ * 2^-10 m (bf16; 2^-14 m in f16), m the largest of 32 positions.  A query row with an
+ * infinity or NaN gets NaN in out and lse if it sees a position, and so does a row
+ * that sees a key or value that is not a number, or whose scores leave float32.
+ * What lies at positions that a row does not see never reaches it, whatever it is. */
 int32_t kv_paged_attention_q4(const spec_kv_attention_desc* desc, const void* q,
                               const void* k_codes, const void* k_scales, const void* v_codes,
                               const float* v_scales, const int32_t* block_table,

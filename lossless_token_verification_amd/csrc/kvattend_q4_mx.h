@@ -7,20 +7,41 @@
 //     S^T = K Q^T     A = key codes from LDS with their block scales
 //     O^T += V^T P^T  A = value codes from LDS, transposed by the read
 // and what stands against the codes is split into pieces that the instructions take
-// at the 4-bit rate: 6-bit numbers (e2m3: 4 significant bits, magnitudes to 7.5)
-// with a power of two per 32.  A piece scaled so that the largest of its 32 is in
-// [2, 4) is off by at most an eighth, the next piece holds that remainder scaled by
-// 32: n pieces are off by 2^-(5n - 1) of the largest at most.
+// at the 4-bit rate: 6-bit numbers (e2m3: 4 significant bits, magnitudes to 7.5, step
+// 1/8 up to 2, 1/4 up to 4, 1/2 above) with a power of two s per 32.  The second piece
+// holds what the first leaves over s / 32, and so on.
+//   Scaled so that the largest of the 32 is in [2, 4) s, a piece leaves an eighth at
+//   most, 4 of the next one's units: n pieces are off by 2^-(5n - 1) of the largest.
+//   Scaled so that it is in (3.75, 7.5] s, a number of 4 s or more leaves up to a
+//   quarter, 8 units where a piece ends at 7.5: two pieces are off by s / 64, 2^-8 of
+//   the number.  Smaller ones are off by 2^-9 of themselves or, below s, by s / 512.
 //   Queries: 3 pieces for bfloat16 (2^-14 of the largest of 32 channels; its 8
-//   bits are held whole down to a 64th of that), 4 for float16 (2^-19).
-//   Weights times their value's scale: 2 pieces for bfloat16 (2^-9 of the largest
-//   of the 32 positions that a lane holds, half a step of that type at its largest),
-//   3 for float16 (2^-14).  The largest is taken anew for every 32 positions, so
-//   that many small weights far from a large one are not lost; the sum of the
-//   weights is taken before, in float32.
+//   bits are held whole down to a 64th of that), 4 for float16 (2^-19), and 4 at
+//   head_dim 64, where two lie side by side in a step of 128 terms.
+//   Weights times their value's scale: 2 pieces for bfloat16 in the second way (2^-8
+//   of itself, half a step of that type), 3 for float16 in the first (2^-14 of the
+//   largest of the 32 positions that a lane holds).  Measured against 64 bits, outputs
+//   are off by 0.0019 to 0.0021 in bfloat16, where rounding them alone gives 0.0017,
+//   and 0.00022 in float16 (0.00021); two pieces in the first way gave 0.0026.  The
+//   largest is taken anew for every 32 positions, so that many small weights far
+//   from a large one are not lost; the sum of the weights is taken before, in float32.
 // The products are exact in the instruction, their sums float32.  Codes hold no
 // infinity: a position that a row does not see has weight 0 and value scale 0, and
 // needs no more care than that.
+//
+// A wavefront takes 16 query rows (of the tokens of one sequence and the heads that
+// share a key head), a workgroup 1 to 4 of them, so that one load of a unit of 128
+// positions (8.75 KB of keys, as much of values, at head_dim 128) serves them all.  Two
+// units lie in LDS, loaded directly.  The split of a weight (32 conversions and their
+// remainders, some 400 instructions a unit) is what no row shares with another.
+// What bounds it, bfloat16, 32 query and 8 key heads of 128:
+//   256 sequences of 512 to 4096 positions, 9 tokens each (719 MB): 160 us, 4.5 TB/s; with
+//     the arithmetic left out the loads take 150 (a short sequence fills its buffers
+//     anew), and the arithmetic of three wavefronts is as long as they are;
+//   4 sequences of 125000, single tokens (553 MB): 98 us, 5.6 TB/s, the loads;
+//   4 prompts of 2200 to 3800 tokens (332 GFLOP): 350 to 390 us; the vector instructions
+//     of softmax and splits (60 % of the cycles), then the matrix instructions (a
+//     quarter), not the loads (150 to 186).
 #pragma once
 
 #include "kvattend_mfma.h"
@@ -133,7 +154,7 @@ __device__ __forceinline__ int swz_q4(int r) {
 }
 
 template <class C>
-__global__ __launch_bounds__((C::W > 4 ? C::W : 4) * kWave) __attribute__((amdgpu_waves_per_eu(C::kPerSimd))) void
+__global__ __launch_bounds__(4 * kWave) __attribute__((amdgpu_waves_per_eu(C::kPerSimd))) void
 attend_q4_kernel(AttendArgs a, Q4Cache cache) {
   using T = typename C::T;
   constexpr int D = C::D, KT = C::KT, ROW = C::ROW, NV = C::NV, RPL = C::RPL, OT = C::OT;
@@ -146,12 +167,7 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int dim = C::kPad ? a.D : D, row_bytes = dim / 2;
-  int x = blockIdx.x / a.kv_heads, h = blockIdx.x - x * a.kv_heads;
-  if (C::kOnce) {
-    const int r = blockIdx.x >> 3, q = r / a.kv_heads;
-    h = r - q * a.kv_heads;
-    x = q * 8 + (blockIdx.x & 7);
-  }
+  const int x = blockIdx.x / a.kv_heads, h = blockIdx.x - x * a.kv_heads;
   AttendItem it;
   if (!attend_find<C::MT, KT, C::W, C::kHeld>(a, x, a.max_slots > 0 && blockIdx.x == 0, plan, it)) return;
   if (it.splits > 1 && h == 0 && tid == 0) attend_slot_info(a, it);
@@ -546,7 +562,7 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
   }
   // whole output rows: turned in LDS (each wavefront its 16 rows), then 16 bytes a lane
   static_assert(4 * 16 * D * 2 <= C::BYTES, "the rows of four wavefronts fit a buffer");
-  char* const turned = (wave < 4 ? sb0 : sb1) + (wave & 3) * 16 * D * 2;
+  char* const turned = sb0 + wave * 16 * D * 2;
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   const bool none = l == 0.0f;
   const int mine = lane & 15;
@@ -574,15 +590,19 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
 
 template <class C>
 void launch_q4_cfg(const AttendArgs& a, const Q4Cache& c, hipStream_t st) {
-  const unsigned items = C::kOnce ? (static_cast<unsigned>(a.grid_items) + 7) / 8 * 8 : a.grid_items;
-  hipLaunchKernelGGL(attend_q4_kernel<C>, dim3(items * a.kv_heads),
-                     dim3(C::W * kWave), 0, st, a, c);
+  const unsigned grid = static_cast<unsigned>(a.grid_items) * a.kv_heads;
+  hipLaunchKernelGGL(attend_q4_kernel<C>, dim3(grid), dim3(C::W * kWave), 0, st, a, c);
 }
 
 template <typename T, int D, bool kPad>
 hipError_t launch_q4_rows(const AttendArgs& a, const Q4Cache& c, int mt, hipStream_t st) {
+  if constexpr (D < 256) {      // (there one wavefront spills: 16 rows go by 32)
+    if (mt == 16) {
+      launch_q4_cfg<Q4Cfg<T, D, kPad, 1>>(a, c, st);
+      return hipGetLastError();
+    }
+  }
   switch (mt) {
-    case 16: launch_q4_cfg<Q4Cfg<T, D, kPad, 1>>(a, c, st); break;
     case 32: launch_q4_cfg<Q4Cfg<T, D, kPad, 2>>(a, c, st); break;
     case 48: launch_q4_cfg<Q4Cfg<T, D, kPad, 3>>(a, c, st); break;
     case 64: launch_q4_cfg<Q4Cfg<T, D, kPad, 4>>(a, c, st); break;

@@ -144,22 +144,33 @@ def bounds(ref, dtype, dim):
     """Error bounds of out [T, H, D] and lse [T, H] by arithmetic.
 
     A query is off by 2^-14 (bfloat16; 2^-19 float16) of the largest of its 32
-    channels, so a score by that times split_abs; its float32 sum of dim products in
-    up to 4 pieces, whose magnitudes add up to 1.1 of the score's, by (dim + 8) 2^-24 1.1
-    score_abs.  A weight is relatively off by twice the error of a score (its own and
-    the largest's), the exponential's steps and the reference's rounding (within 16
-    log2 units).  A weight times its scale is off by 2^-9 (bfloat16; 2^-14 float16)
-    of the largest of its lane's 32 positions.  Float32 sums over n keys add n 2^-24
-    relative to the absolute sum, joins and the division 16 steps; the output is
-    rounded once to its type."""
+    channels, so a score by that times split_abs.  Its float32 sum starts from the
+    row's reference, which is within 8 log2 units of a score, and takes dim products
+    in up to 4 pieces whose magnitudes add up to 1.1 of the score's: every partial sum
+    is below 2.1 score_abs + 8 ln 2, and dim + 8 of them round by 2^-24 each.  A
+    weight is relatively off by twice the error of a score (its own and the
+    largest's), the exponential's steps and the reference's rounding (within 16 log2
+    units).
+
+    A weight times its scale, x, in two pieces (bfloat16) over a unit s, where the
+    largest of its lane's 32 positions is in (3.75 s, 7.5 s].  A piece's step is s / 2
+    from 4 s on, s / 4 from 2 s on, s / 8 below that.  x of 4 s or more leaves s / 4 at
+    most, 8 units of the second piece, which ends at 7.5: off by half of one of these,
+    s / 64 <= 2^-8 x.  x in [2 s, 4 s) leaves s / 8, 4 of them, and is off by an eighth
+    of one, s / 256 <= 2^-9 x; below that it leaves s / 16, 2 of them, off by a
+    sixteenth, s / 512, which is 2^-10.9 of the largest at most.  Three pieces
+    (float16), the largest in [2 s, 4 s): 2^-14 of it.  Float32 sums over n keys add
+    n 2^-24 relative to the absolute sum, joins and the division 16 steps; the output
+    is rounded once to its type."""
     half = torch.finfo(C.DT[dtype]).eps / 2
-    split, piece = (2.0 ** -14, 2.0 ** -9) if dtype == "bf16" else (2.0 ** -19, 2.0 ** -14)
+    split = 2.0 ** (-14 if dtype == "bf16" else -19)
+    own, piece = (2.0 ** -8, 2.0 ** -9 / 3.75) if dtype == "bf16" else (0.0, 2.0 ** -14)
     u = 2.0 ** -24
     n = ref["keys"][..., None]
-    e_s = split * ref["split_abs"] + 1.1 * (dim + 8) * u * ref["score_abs"]
+    e_s = split * ref["split_abs"] + (dim + 8) * u * (2.1 * ref["score_abs"] + 8 * math.log(2))
     e_w = 2 * e_s + 24 * u
     rel = 2 * np.expm1(e_w)[..., None] + (n + 16) * u
-    tol = rel * ref["weight_abs"] + piece * (1 + rel) * ref["piece_abs"]
+    tol = (rel + own * (1 + rel)) * ref["weight_abs"] + piece * (1 + rel) * ref["piece_abs"]
     tol = tol * 1.01 + half * (np.abs(ref["out"]) + tol)
     if dtype == "f16":
         tol = tol + 2.0 ** -25          # subnormal outputs
