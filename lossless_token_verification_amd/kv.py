@@ -349,6 +349,8 @@ def _rotation(desc, q, positions, cos_sin, interleaved, out, dev):
     pc = _tensor(cos_sin, "cos_sin", torch.float32, (rows, rot), dev)
     pp = _tensor(positions, "positions", torch.int32, (T,), dev)
     if q is None:
+        if out is not None:
+            raise ValueError("out needs q")
         return None, pp, pc, None, None
     desc.q_stride = _row_stride(q, "q")
     if q.shape[0] != T or q.shape[2] != desc.head_dim or _CODES.get(q.dtype) != desc.dtype or \
