@@ -94,8 +94,10 @@ sv::RotaryArgs rotary_args(const spec_kv_rotary_desc& d, const RotaryPlan& p, bo
   return a;
 }
 
+// Row t.  (Unsigned: rows that no memory holds have no address, and wrap.)
 const void* at(const void* p, int64_t t, int64_t stride, int es) {
-  return p ? static_cast<const char*>(p) + t * stride * es : nullptr;
+  const uint64_t bytes = static_cast<uint64_t>(t) * static_cast<uint64_t>(stride) * es;
+  return p ? reinterpret_cast<const void*>(reinterpret_cast<uintptr_t>(p) + bytes) : nullptr;
 }
 
 void set_rows(sv::RotaryArgs* a, const spec_kv_rotary_desc& d, const RotaryPlan& p, int64_t t,
