@@ -176,19 +176,14 @@ def _key_codes(x):
     byte = (torch.where(part > 0.875, power + 1, power) - 3 + 127).clamp(0, 254)
     byte = torch.where(top > 0, byte, 0)
     byte = torch.where(torch.isfinite(top), byte, 255)
-    codes = _codes(g / _power(byte)[..., None])
+    unit = torch.ldexp(torch.ones((), dtype=torch.float64, device=x.device), byte - 127)
+    codes = _codes(g / unit[..., None].float().clamp(min=2.0 ** -126))
     return codes.view(x.shape), byte.to(torch.uint8)
-
-
-def _power(byte):
-    """2^(byte - 127) in float32."""
-    bits = torch.where(byte == 0, 1 << 22, byte.int() << 23)
-    return torch.where(byte == 255, math.nan, bits.int().view(torch.float32))
 
 
 def _value_codes(x):
     """Codes and scales of value rows [..., dim] in float32."""
-    scale = (x.abs().amax(-1).double() / 6).float().bfloat16().float()
+    scale = (x.abs().amax(-1) / 6).bfloat16().float()
     bad = ~torch.isfinite(scale)
     level = x.double() / torch.where(scale > 0, scale, math.inf)[..., None]
     return _codes(level), torch.where(bad, math.nan, scale)
@@ -221,7 +216,9 @@ def _unpacked(packed):
 def _key_scales(packed, byte):
     """The power of two of every channel."""
     groups = packed.shape[-1] // 16
-    return _power(byte[..., :groups]).repeat_interleave(32, -1)
+    b = byte[..., :groups].int()
+    unit = torch.where(b == 255, math.nan, torch.ldexp(torch.ones((), device=b.device), b - 127))
+    return unit.repeat_interleave(32, -1)
 
 
 def _empty_cache(blocks, kv, block, dim):
@@ -466,7 +463,7 @@ def exact(case, seed):
         unit = torch.where(top > 7 * unit, unit * 2, torch.where(top <= 3.5 * unit, unit / 2, unit))
         k = torch.where(mine, (_exact_level(groups / unit) * unit).view(k.shape), 0.0)
         v = s["v"].double()
-        unit = (v.abs().amax(-1, keepdim=True) / 6).float().bfloat16().double()
+        unit = (s["v"].float().abs().amax(-1, keepdim=True) / 6).bfloat16().double()
         v = torch.where(mine, _exact_level(v / unit) * unit, 0.0)
         return dict(q=q, k=k, v=v) if s["rot"] else dict(k=k, v=v)
     ctx, new = _lengths(case)
