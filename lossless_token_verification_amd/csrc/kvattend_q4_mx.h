@@ -359,9 +359,10 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
   // The scores come out less the reference of their row (they start from its
   // negative), which lies kSlack above the row's largest score where it moved last:
   // 2^-kSlack is the largest weight then, and a lane's 32 add up to an eighth at most.
-  // It moves again when a lane's weights add up to more than 1, which takes no maximum
-  // over the scores in the other units.  most: that limit, or -1 until the row sees a
-  // position (its reference is 0 till then), so that any sum is over it.
+  // It moves again when the weights of one of the row's four lanes add up to more than
+  // 1, which takes no maximum over the scores in the other units.  The other rows of the
+  // tile have no part in that: theirs stay, and so do their bits.  most: that limit, or -1
+  // until the row sees a position (its reference is 0 till then), so that any sum is over it.
   constexpr float kMost = 1.0f;
   f32x4 o[OT];
   float ref = 0.0f, most = -1.0f, l = 0.0f;
@@ -451,8 +452,9 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
     }
     return sum;
   };
-  // Moves the references to these scores (less the old ones).
-  auto move_up = [&](f32x4 (&st)[8]) {
+  // Moves the references of the rows that are over their limit to these scores (less the
+  // old ones).
+  auto move_up = [&](f32x4 (&st)[8], bool over) {
     float mx = st[0][0];
 #pragma unroll
     for (int t = 0; t < 8; ++t)
@@ -461,7 +463,7 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
     mx = max_across<16>(mx);
     mx = max_across<32>(mx);
     const bool first = most < 0.0f;           // the row has seen nothing before
-    const bool move = mx > (first ? -INFINITY : -kSlack);
+    const bool move = over && mx > -INFINITY;
     const float up = move ? mx + kSlack : 0.0f;
     const float f = move && first ? 0.0f : __builtin_amdgcn_exp2f(-up);
     most = move ? kMost : most;
@@ -479,12 +481,14 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
     f32x4 st[8];
     f32x16 x0, x1;
     scores(sb, u, n, st, masked, dead);
-    if (decltype(kFirst)::value) move_up(st);
+    if (decltype(kFirst)::value) move_up(st, true);
     float sum = weigh(sb, st, x0, x1);
-    if (!decltype(kFirst)::value && __any(sum > most)) {
+    const uint64_t lanes = decltype(kFirst)::value ? 0 : __ballot(sum > most);
+    if (lanes != 0) {
       asm volatile("" ::: "memory");        // (formed again: not held through the other units)
       scores(sb, u, n, st, masked, dead);
-      move_up(st);
+      const uint64_t rows = lanes | lanes >> 32;
+      move_up(st, ((rows | rows >> 16) >> (lane & 15)) & 1);
       sum = weigh(sb, st, x0, x1);
     }
     asm volatile("" : "+v"(sum));       // formed here: 32 weights need not be held until later
