@@ -287,8 +287,9 @@ size_t kv_paged_attention_q4_workspace_bytes(const spec_kv_attention_desc* desc)
  * num_blocks * block_size * kv_heads < 2^32.
  * Products on the matrix cores, on the codes as they lie, float32 sums.  What stands
  * against the codes is split into pieces of 4 significant bits with a power of two
- * per 32.  A query's pieces add up to it within 2^-14 of the largest of 32 channels
- * (bf16; 2^-19 in f16).  A softmax weight times its value's scale, x: within 2^-8 |x| +
+ * per 32.  A query's pieces add up to it: channels of a 128th of the largest of their
+ * 32 (f16: of a 512th) are held whole, smaller ones within 2^-14 of the largest (f16:
+ * 2^-19).  A softmax weight times its value's scale, x: within 2^-8 |x| +
  * 2^-10 m (bf16; 2^-14 m in f16), m the largest of 32 positions (2^-104 at least, where
  * the row's largest weight is 2^-8).  A query row with an
  * infinity or NaN gets NaN in out and lse if it sees a position, and so does a row

@@ -15,9 +15,12 @@
 //   Scaled so that it is in (3.75, 7.5] s, a number of 4 s or more leaves up to a
 //   quarter, 8 units where a piece ends at 7.5: two pieces are off by s / 64, 2^-8 of
 //   the number.  Smaller ones are off by 2^-9 of themselves or, below s, by s / 512.
-//   Queries: 3 pieces for bfloat16 (2^-14 of the largest of 32 channels; its 8
-//   bits are held whole down to a 64th of that), 4 for float16 (2^-19), and 4 at
-//   head_dim 64, where two lie side by side in a step of 128 terms.
+//   Queries, as they are: 3 pieces for bfloat16 (2^-14 of the largest of 32 channels;
+//   its 8 bits are held whole down to a 128th of that), 4 for float16 (2^-19; 11 bits
+//   down to a 512th), and 4 at head_dim 64, where two lie side by side in a step of
+//   128 terms.  The scale is applied to their products, in the weights' exponent: the
+//   pieces of a query times 24 bits of a scale held none of it whole, and every lse was
+//   off by that.
 //   Weights times their value's scale: 2 pieces for bfloat16 in the second way (2^-8
 //   of itself, half a step of that type), 3 for float16 in the first (2^-14 of the
 //   largest of the 32 positions that a lane holds).  Measured against 64 bits, outputs
@@ -86,22 +89,22 @@ __device__ __forceinline__ f32x32 from_fp6(u32x6 x, float s) {
 }
 
 // The N pieces of 32 numbers, even ones in x0 and odd ones in x1, the largest of
-// magnitude `top` (as bits).  add: what the scales' exponents are raised by.  Two
-// pieces are scaled so that the largest is in (3.75, 7.5], more so that it is in [2, 4).
+// magnitude `top` (as bits).  Two pieces are scaled so that the largest is in (3.75, 7.5],
+// more so that it is in [2, 4).
 // Numbers below 2^-104 lose bits (the first piece's scale is 2^-103 at least, so that the
 // last one's is a number).
 template <int N>
-__device__ __forceinline__ void split_pieces(f32x16 x0, f32x16 x1, uint32_t top, int add,
-                                             u32x6 (&piece)[N], int (&scale)[N]) {
+__device__ __forceinline__ void split_pieces(f32x16 x0, f32x16 x1, uint32_t top, u32x6 (&piece)[N],
+                                             int (&scale)[N]) {
 #pragma clang fp contract(off)
   const int e = N == 2 ? static_cast<int>((top + 0xfffffu) >> 23) - 2 : static_cast<int>(top >> 23) - 1;
   const int b = max(e, 24);
 #pragma unroll
   for (int p = 0; p < N; ++p) {
-    const float s = __uint_as_float(static_cast<uint32_t>(min(b, 254) - 5 * p) << 23);
+    const float s = __uint_as_float(static_cast<uint32_t>(b - 5 * p) << 23);
     piece[p] = to_fp6(x0, x1, s);
     // infinity or NaN among them: NaN
-    scale[p] = top >= 0x7f800000u || b + add > 254 ? 255 : max(b + add - 5 * p, 0);
+    scale[p] = top >= 0x7f800000u ? 255 : b - 5 * p;
     if (p + 1 < N) {
       const f32x32 y = from_fp6(piece[p], s);
 #pragma unroll
@@ -320,10 +323,6 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
   u32x6 qf[HALVES][QS];
   int qs[HALVES];        // a byte for each step's pieces
   {
-    // scores in log2 units: the factor's significand goes into the queries, its
-    // exponent into their scales
-    int factor_exp;
-    const float factor = frexpf(a.scale * kLog2e, &factor_exp);
 #pragma unroll
     for (int hf = 0; hf < HALVES; ++hf) {
       f32x16 x0, x1;
@@ -334,15 +333,15 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
         const t8 v = __builtin_bit_cast(t8, raw[hf][i]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          x0[i * 4 + j] = static_cast<float>(v[2 * j]) * factor;
-          x1[i * 4 + j] = static_cast<float>(v[2 * j + 1]) * factor;
+          x0[i * 4 + j] = static_cast<float>(v[2 * j]);
+          x1[i * 4 + j] = static_cast<float>(v[2 * j + 1]);
           top = max(top, __float_as_uint(x0[i * 4 + j]) & 0x7fffffffu);
           top = max(top, __float_as_uint(x1[i * 4 + j]) & 0x7fffffffu);
         }
       }
       u32x6 piece[PQ];
       int scale[PQ];
-      split_pieces<PQ>(x0, x1, top, factor_exp, piece, scale);
+      split_pieces<PQ>(x0, x1, top, piece, scale);
       qs[hf] = 0;
 #pragma unroll
       for (int s = 0; s < QS; ++s) {
@@ -356,14 +355,15 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
       }
     }
   }
-  // The scores come out less the reference of their row (they start from its
-  // negative), which lies kSlack above the row's largest score where it moved last:
-  // 2^-kSlack is the largest weight then, and a lane's 32 add up to an eighth at most.
+  // Weights are 2^(factor * product - ref): the reference of a row, in log2 units, lies
+  // kSlack above its largest score where it moved last: 2^-kSlack is the largest weight
+  // then, and a lane's 32 add up to an eighth at most.
   // It moves again when the weights of one of the row's four lanes add up to more than
   // 1, which takes no maximum over the scores in the other units.  The other rows of the
   // tile have no part in that: theirs stay, and so do their bits.  most: that limit, or -1
   // until the row sees a position (its reference is 0 till then), so that any sum is over it.
   constexpr float kMost = 1.0f;
+  const float factor = a.scale * kLog2e;
   f32x4 o[OT];
   float ref = 0.0f, most = -1.0f, l = 0.0f;
 #pragma unroll
@@ -382,9 +382,8 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
   const int vkey = 64 * (n16 & 1) + 16 * (n16 >> 3) + 4 * g + ((n16 >> 1) & 3);
   const int voff = vkey * ROW + (swz_q4<D>(vkey) << 4);
 
-  // The scores of unit u, less the references: st[t][r] of position 16 t + r and the
-  // lane's part 4 g, -inf where it is not seen (masked: there may be such; dead: their
-  // bits 4 t + r).
+  // The products of unit u: st[t][r] of position 16 t + r and the lane's part 4 g, -inf
+  // where it is not seen (masked: there may be such; dead: their bits 4 t + r).
   auto scores = [&](const char* sb, int u, int n, f32x4 (&st)[8], bool masked,
                     uint32_t& dead) {
 #pragma unroll
@@ -397,9 +396,9 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
         ks[t] = static_cast<uint8_t>(sb[C::kKS + hf * KT * 4 + ksoff + t * 64]);
         if (C::kPad && (hf * 4 + kgroup) * 32 >= dim) ks[t] = 0;
       }
-      const f32x4 from = {-ref, -ref, -ref, -ref};
 #pragma unroll
-      for (int t = 0; t < 8; ++t) st[t] = mma_q4<0>(k[t], ks[t], qf[hf][0], qs[hf], hf ? st[t] : from);
+      for (int t = 0; t < 8; ++t)
+        st[t] = mma_q4<0>(k[t], ks[t], qf[hf][0], qs[hf], hf ? st[t] : f32x4{0.0f, 0.0f, 0.0f, 0.0f});
 #pragma unroll
       for (int t = 0; t < 8; ++t) st[t] = mma_q4<1>(k[t], ks[t], qf[hf][1], qs[hf], st[t]);
       if constexpr (QS > 2) {
@@ -444,7 +443,7 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
       const f32x4 vs = *reinterpret_cast<const f32x4*>(sb + C::kVS + (t * 16 + 4 * g) * 4);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const float p = __builtin_amdgcn_exp2f(st[t][r]);
+        const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(st[t][r], factor, -ref));
         sum += p;
         if (t < 4) x0[t * 4 + r] = p * vs[r];
         else x1[(t - 4) * 4 + r] = p * vs[r];
@@ -452,9 +451,8 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
     }
     return sum;
   };
-  // Moves the references of the rows that are over their limit to these scores (less the
-  // old ones).
-  auto move_up = [&](f32x4 (&st)[8], bool over) {
+  // Moves the references of the rows that are over their limit to these products.
+  auto move_up = [&](const f32x4 (&st)[8], bool over) {
     float mx = st[0][0];
 #pragma unroll
     for (int t = 0; t < 8; ++t)
@@ -462,17 +460,16 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
       for (int r = 0; r < 4; ++r) mx = fmaxf(mx, st[t][r]);
     mx = max_across<16>(mx);
     mx = max_across<32>(mx);
-    const bool first = most < 0.0f;           // the row has seen nothing before
+    mx *= factor;
     const bool move = over && mx > -INFINITY;
-    const float up = move ? mx + kSlack : 0.0f;
-    const float f = move && first ? 0.0f : __builtin_amdgcn_exp2f(-up);
+    const float to = move ? mx + kSlack : ref;
+    // (0 where the row has seen nothing before)
+    const float f = move && most < 0.0f ? 0.0f : __builtin_amdgcn_exp2f(ref - to);
     most = move ? kMost : most;
-    ref += up;
+    ref = to;
     l *= f;
 #pragma unroll
     for (int t = 0; t < OT; ++t) o[t] *= f;
-#pragma unroll
-    for (int t = 0; t < 8; ++t) st[t] -= up;
   };
   // Unit u, the n-th of the item; kFirst: n is 0.
   auto compute = [&](auto kFirst, const char* sb, int u, int n) {
@@ -506,7 +503,7 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
     l += sum;
     u32x6 piece[PP];
     int scale[PP];
-    split_pieces<PP>(x0, x1, top, 0, piece, scale);
+    split_pieces<PP>(x0, x1, top, piece, scale);
     const int vo = fresh(voff);
 #pragma unroll
     for (int t0 = 0; t0 < OT; t0 += 4) {
