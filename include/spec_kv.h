@@ -289,9 +289,8 @@ size_t kv_paged_attention_q4_workspace_bytes(const spec_kv_attention_desc* desc)
  * against the codes is split into pieces of 4 significant bits with a power of two
  * per 32.  A query's pieces add up to it: channels of a 128th of the largest of their
  * 32 (f16: of a 512th) are held whole, smaller ones within 2^-14 of the largest (f16:
- * 2^-19).  A softmax weight times its value's scale, x: within 2^-8 |x| +
- * 2^-10 m (bf16; 2^-14 m in f16), m the largest of 32 positions (2^-104 at least, where
- * the row's largest weight is 2^-8).  A query row with an
+ * 2^-19).  A softmax weight times its value's scale: within 2^-14 of the largest of 32
+ * positions (2^-104 at least, where the row's largest weight is 2^-8).  A query row with an
  * infinity or NaN gets NaN in out and lse if it sees a position, and so does a row
  * that sees a key or value that is not a finite number, or whose scores leave float32.
  * What lies at positions that a row does not see never reaches it, whatever it is. */

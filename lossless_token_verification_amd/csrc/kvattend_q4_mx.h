@@ -12,22 +12,19 @@
 // holds what the first leaves over s / 32, and so on.
 //   Scaled so that the largest of the 32 is in [2, 4) s, a piece leaves an eighth at
 //   most, 4 of the next one's units: n pieces are off by 2^-(5n - 1) of the largest.
-//   Scaled so that it is in (3.75, 7.5] s, a number of 4 s or more leaves up to a
-//   quarter, 8 units where a piece ends at 7.5: two pieces are off by s / 64, 2^-8 of
-//   the number.  Smaller ones are off by 2^-9 of themselves or, below s, by s / 512.
 //   Queries, as they are: 3 pieces for bfloat16 (2^-14 of the largest of 32 channels;
 //   its 8 bits are held whole down to a 128th of that), 4 for float16 (2^-19; 11 bits
 //   down to a 512th), and 4 at head_dim 64, where two lie side by side in a step of
 //   128 terms.  The scale is applied to their products, in the weights' exponent: the
 //   pieces of a query times 24 bits of a scale held none of it whole, and every lse was
 //   off by that.
-//   Weights times their value's scale: 2 pieces for bfloat16 in the second way (2^-8
-//   of itself, half a step of that type), 3 for float16 in the first (2^-14 of the
-//   largest of the 32 positions that a lane holds).  Measured against 64 bits, outputs
-//   are off by 0.0019 to 0.0021 in bfloat16, where rounding them alone gives 0.0017,
-//   and 0.00022 in float16 (0.00021); two pieces in the first way gave 0.0026.  The
-//   largest is taken anew for every 32 positions, so that many small weights far
-//   from a large one are not lost; the sum of the weights is taken before, in float32.
+//   Weights times their value's scale: 3 pieces (2^-14 of the largest of the 32
+//   positions that a lane holds).  Two would be faster in bfloat16 (256 windows of 9
+//   tokens 173 us against 194, four prompts 359 against 405), but end at 2^-11 of the
+//   largest: 31 weights just below that were missing from the output, 1.4 % of it, and
+//   not from the sum of the weights.  The largest is taken anew for every 32 positions, so
+//   that many small weights far from a large one are not lost; the sum of the weights is
+//   taken before, in float32.
 // The products are exact in the instruction, their sums float32.  Codes hold no
 // infinity: a position that a row does not see has weight 0 and value scale 0, and
 // needs no more care than that.
@@ -89,16 +86,13 @@ __device__ __forceinline__ f32x32 from_fp6(u32x6 x, float s) {
 }
 
 // The N pieces of 32 numbers, even ones in x0 and odd ones in x1, the largest of
-// magnitude `top` (as bits).  Two pieces are scaled so that the largest is in (3.75, 7.5],
-// more so that it is in [2, 4).
-// Numbers below 2^-104 lose bits (the first piece's scale is 2^-103 at least, so that the
+// magnitude `top` (as bits), scaled so that it is in [2, 4).  Numbers below 2^-104 lose bits (the first piece's scale is 2^-103 at least, so that the
 // last one's is a number).
 template <int N>
 __device__ __forceinline__ void split_pieces(f32x16 x0, f32x16 x1, uint32_t top, u32x6 (&piece)[N],
                                              int (&scale)[N]) {
 #pragma clang fp contract(off)
-  const int e = N == 2 ? static_cast<int>((top + 0xfffffu) >> 23) - 2 : static_cast<int>(top >> 23) - 1;
-  const int b = max(e, 24);
+  const int b = max(static_cast<int>(top >> 23) - 1, 24);
 #pragma unroll
   for (int p = 0; p < N; ++p) {
     const float s = __uint_as_float(static_cast<uint32_t>(b - 5 * p) << 23);
@@ -130,7 +124,7 @@ struct Q4Cfg {
   static constexpr int D = D_, W = W_, KT = kQ4KT, MT = 16 * W;
   static constexpr bool kBf = std::is_same<T, __bf16>::value;
   // pieces; at D = 64 two of a query's lie side by side in one step
-  static constexpr int PQ = D == 64 || !kBf ? 4 : 3, PP = kBf ? 2 : 3;
+  static constexpr int PQ = D == 64 || !kBf ? 4 : 3, PP = 3;
   static constexpr int HALVES = D == 256 ? 2 : 1;          // steps along a row
   static constexpr int QS = D == 64 ? PQ / 2 : PQ;         // steps of a half
   static constexpr int ROW = D / 2;                        // bytes of a row of codes

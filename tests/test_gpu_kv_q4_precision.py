@@ -75,3 +75,66 @@ def test_scores_hold_queries_whole(sv, byte, scale, dim, dtype):
     print(f"{(off / bound).max():.3f} of the bound")
     assert (off <= bound).all(), (off / bound).max()
     assert (C.to64(r["out"]) == 1.0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dim", [32, 64, 128, 224, 256])
+@pytest.mark.parametrize("steps", [9.0, 10.95, 13.0])
+def test_many_weights_far_below_one(sv, steps, dim, dtype):
+    """A token over 128 or 640 positions with one key in 32 that outweighs each of the
+    others by 2^steps; all values are 6 units.  The others' share stays in the output as
+    in the sum of the weights: the output is 6 units.
+
+    A weight times its scale is off by 2^-14 of the largest of its lane's 32 at most, a
+    lane's 32 by 2^-9 of it, and the sum of the weights is not less than that largest.  The
+    rest of it is float32 (640 sums and some steps of 2^-24, and the exponential's), the
+    output is rounded once."""
+    half = torch.finfo(C.DT[dtype]).eps / 2
+    for L in (128, 640):
+        n, heads = L // 16, 4
+        unit = 0.9453125                  # times a weight of a power of two just over 3.75 / 4
+        c = dict(k_codes=torch.zeros((n, 1, 16, dim // 2), dtype=torch.uint8),
+                 k_scales=torch.full((n, 1, 16, -(-dim // 128) * 4), 127, dtype=torch.uint8),
+                 v_codes=torch.full((n, 1, 16, dim // 2), 0x77, dtype=torch.uint8),
+                 v_scales=torch.full((n, 1, 16), unit))
+        c["k_codes"][0::8, 0, 0::4, 0] = 0x07     # of each lane's 32 of 128 positions the first
+        q = torch.zeros((1, heads, dim), dtype=C.DT[dtype])
+        q[:, :, 0] = 1.0
+        case = dict(q=q, cache=c, block_table=torch.arange(n, dtype=torch.int32)[None],
+                    seq_lens=torch.tensor([L], dtype=torch.int32),
+                    cu_tokens=torch.tensor([0, 1], dtype=torch.int32))
+        gpu = Q.on_gpu(case)
+        r = sv.kv_paged_attention_q4(*[gpu[m] for m in Q.NAMES], lse=True,
+                                     scale=steps * math.log(2) / 6)
+        torch.cuda.synchronize()
+        off = (np.abs(C.to64(r["out"]) / (6 * unit) - 1)).max()
+        bound = 2.0 ** -9 + half * (1 + 2.0 ** -9) + 700 * U
+        print(f"{L}: {off:.2e}, {off / bound:.3f} of the bound")
+        assert off <= bound, (L, off, bound)
+        lse = steps * math.log(2) + math.log((L // 32) * (1 + 31 * 2.0 ** -steps))
+        assert np.abs(C.to64(r["lse"]) - lse).max() <= (L + 80) * U * 12
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dim,ctx,new,heads,kv", [
+    (64, [700, 30], [3, 40], 8, 2), (128, [1500, 0], [9, 100], 8, 2), (256, [300, 1], [5, 33], 4, 4),
+    (96, [2500], [1], 6, 2)])
+def test_outputs_within_three_pieces(sv, dim, ctx, new, heads, kv, dtype):
+    """The bounds of tests/kvq4cases.py with 2^-14 of the largest of a lane's 32 positions
+    for the weights of either type."""
+    case = Q.attend_case(ctx, new, heads, kv, dim, 16, dtype, seed=70)
+    gpu = Q.on_gpu(case)
+    r = sv.kv_paged_attention_q4(*[gpu[m] for m in Q.NAMES], lse=True)
+    torch.cuda.synchronize()
+    ref = Q.reference(case)
+    half = torch.finfo(C.DT[dtype]).eps / 2
+    e_s = 2.0 ** (-14 if dtype == "bf16" else -19) * ref["split_abs"] + \
+        (dim + 8) * U * (2.1 * ref["score_abs"] + 8 * math.log(2))
+    rel = 2 * np.expm1(2 * e_s + 24 * U)[..., None] + (ref["keys"][..., None] + 16) * U
+    tol = rel * ref["weight_abs"] + 2.0 ** -14 * (1 + rel) * ref["piece_abs"]
+    tol = tol * 1.01 + half * (np.abs(ref["out"]) + tol) + 2.0 ** -25
+    off = np.abs(C.to64(r["out"]) - ref["out"])
+    rounded = np.abs(torch.from_numpy(ref["out"]).to(C.DT[dtype]).double().numpy() - ref["out"])
+    print(f"{(off / tol).max():.3f} of the bound, {np.sqrt((off ** 2).sum() / (rounded ** 2).sum()):.3f} "
+          "times the rounding alone")
+    assert (off <= tol).all(), (off / tol).max()
