@@ -109,7 +109,7 @@ void set_rows(sv::RotaryArgs* a, const spec_kv_rotary_desc& d, const RotaryPlan&
   a->k = at(k, t, p.k_stride, es);
   a->v = at(v, t, p.v_stride, es);
   a->q_out = const_cast<void*>(at(q_out, t, p.q_out_stride, es));
-  a->positions = positions + t;
+  a->positions = positions ? positions + t : nullptr;   // (NULL without a rotation)
   a->cos_sin = cos_sin;
   a->slots = slot_map + t;
 }
