@@ -238,9 +238,9 @@ int32_t kv_cache_append_q4(const spec_kv_rotary_desc* desc, const void* q, const
   a.bs = sv::make_fast_div(static_cast<uint32_t>(d.block_size));
   a.heads = sv::make_fast_div(static_cast<uint32_t>(d.kv_heads));
   a.cos_sin = cos_sin;
-  const int64_t most = std::max<int64_t>(static_cast<int64_t>(a.kv_heads) * a.row_lanes, qa.token_units);
-  if (most == 0) return SV_OK;
-  const int64_t step = INT32_MAX / most;     // of either part, below 2^31 threads
+  const int64_t token = static_cast<int64_t>(a.kv_heads) * a.row_lanes + qa.token_units;
+  if (token == 0) return SV_OK;
+  const int64_t step = INT32_MAX / token;    // both parts of a launch below 2^31 threads together
   for (int64_t t = 0; t < d.tokens; t += step) {
     const int64_t n = std::min<int64_t>(step, d.tokens - t);
     set_rows(&qa, d, p, t, n, q, k, v, positions, cos_sin, slot_map, q_out);

@@ -46,6 +46,10 @@ hipError_t launch_rotary(const RotaryArgs& a, int, bool, hipStream_t) {
 hipError_t launch_q4_append(const Q4RowsArgs& a, const RotaryArgs& q, int, bool, bool, hipStream_t) {
   take(q.q, g_queries, q.q_stride * 2, "q");
   take(a.k, true, a.k_stride * 2, "k");
+  // workgroups of 256 threads for the rows, then for the queries, fewer than 2^32 threads
+  const int64_t per = 256 / a.row_lanes;
+  const int64_t groups = (int64_t{a.T} * a.kv_heads + per - 1) / per + (int64_t{q.T} * q.token_units + 255) / 256;
+  if (groups * 256 >= int64_t{1} << 32) die("threads of a launch", groups, a.T);
   rows(a.T, a.positions, a.slots);
   return hipSuccess;
 }
@@ -65,11 +69,11 @@ int main() {
   float* const F = reinterpret_cast<float*>(P);
   int64_t* const L = reinterpret_cast<int64_t*>(P);
   long parts = 0;
-  for (int32_t T : {1, 20000000, 500000000, INT32_MAX})
-    for (int32_t kv : {1, 8, 64})
+  for (int32_t T : {1, 20000000, 33554431, 500000000, INT32_MAX})
+    for (int32_t kv : {1, 4, 8, 64})
       for (int32_t heads : {0, 8, 64})
         for (int32_t dim : {32, 128, 256})
-          for (int32_t rot : {0, 32})
+          for (int32_t rot : {0, 32, dim})
             for (int32_t nb : {0, 4096}) {
               spec_kv_rotary_desc d{};
               d.tokens = T, d.heads = heads, d.kv_heads = kv, d.head_dim = dim, d.block_size = 16;
