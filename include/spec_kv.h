@@ -232,7 +232,8 @@ typedef struct {
  *               position's angles
  *   slot_map    [T] device int64, as for kv_cache_append
  *   q_out       [T, heads, head_dim] device; may be q itself (same stride), and
- *               must not overlap it otherwise
+ *               must not overlap it otherwise (refused, unless the strides differ
+ *               too)
  * A row whose position is not in the table is skipped: neither its query nor its
  * key and value are written.  A row without a slot is written to q_out alone.
  * Whole 16-byte vectors that turn together (R a multiple of 16 bytes, of twice

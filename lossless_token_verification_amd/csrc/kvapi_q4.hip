@@ -44,14 +44,31 @@ int32_t check_rotary(const spec_kv_rotary_desc* desc, bool q4, RotaryPlan* p) {
   return check_stride(&p->q_out_stride, q_row, "q_out_stride");
 }
 
+// Queries are turned in place, row by row, or to rows that do not overlap them (rows of
+// two strides from different places on are the caller's).
+int32_t check_in_place(const spec_kv_rotary_desc& d, const RotaryPlan& p, const void* q, const void* q_out) {
+  const uint64_t from = reinterpret_cast<uintptr_t>(q), to = reinterpret_cast<uintptr_t>(q_out);
+  const uint64_t by = from < to ? to - from : from - to, es = dtype_bytes(d.dtype);
+  const uint64_t row = static_cast<uint64_t>(d.heads) * d.head_dim * es;
+  const bool alike = d.tokens == 1 || p.q_stride == p.q_out_stride;
+  if (by == 0)
+    return alike ? SV_OK : fail(SV_ERR_INVALID_ARG, "q_out is q with another stride");
+  if (!alike) return SV_OK;
+  const uint64_t stride = p.q_stride * es, rows = by / stride, rest = by % stride, last = d.tokens - 1;
+  if ((rows <= last && rest < row) || (rows < last && stride - rest < row))
+    return fail(SV_ERR_INVALID_ARG, "q_out overlaps q");
+  return SV_OK;
+}
+
 // The rows' part of the pointer checks.
-int32_t check_rows(const spec_kv_rotary_desc& d, const void* q, const void* k, const void* v,
-                   const int32_t* positions, const float* cos_sin, const int64_t* slot_map,
-                   const void* q_out) {
+int32_t check_rows(const spec_kv_rotary_desc& d, const RotaryPlan& p, const void* q, const void* k,
+                   const void* v, const int32_t* positions, const float* cos_sin,
+                   const int64_t* slot_map, const void* q_out) {
   const int es = dtype_bytes(d.dtype);
   const bool any = d.tokens > 0, turn = any && d.rotary_dim > 0;
   SV_TRY(check_ptr(q, any && d.heads > 0, es, "q"));
   SV_TRY(check_ptr(q_out, any && d.heads > 0, es, "q_out"));
+  if (any && d.heads > 0) SV_TRY(check_in_place(d, p, q, q_out));
   SV_TRY(check_ptr(k, any, es, "k"));
   SV_TRY(check_ptr(v, any, es, "v"));
   SV_TRY(check_ptr(positions, turn, 4, "positions"));
@@ -182,7 +199,7 @@ int32_t kv_cache_append_rotary(const spec_kv_rotary_desc* desc, const void* q, c
   RotaryPlan p;
   SV_TRY(check_rotary(desc, false, &p));
   const spec_kv_rotary_desc& d = *desc;
-  SV_TRY(check_rows(d, q, k, v, positions, cos_sin, slot_map, q_out));
+  SV_TRY(check_rows(d, p, q, k, v, positions, cos_sin, slot_map, q_out));
   const int es = dtype_bytes(d.dtype), vec = 16 / es;
   SV_TRY(check_ptr(k_cache, d.tokens > 0 && d.num_blocks > 0, es, "k_cache"));
   SV_TRY(check_ptr(v_cache, d.tokens > 0 && d.num_blocks > 0, es, "v_cache"));
@@ -212,7 +229,7 @@ int32_t kv_cache_append_q4(const spec_kv_rotary_desc* desc, const void* q, const
   RotaryPlan p;
   SV_TRY(check_rotary(desc, true, &p));
   const spec_kv_rotary_desc& d = *desc;
-  SV_TRY(check_rows(d, q, k, v, positions, cos_sin, slot_map, q_out));
+  SV_TRY(check_rows(d, p, q, k, v, positions, cos_sin, slot_map, q_out));
   SV_TRY(check_q4_cache(d.tokens > 0 && d.num_blocks > 0, k_codes, k_scales, v_codes, v_scales));
   const int es = dtype_bytes(d.dtype), vec = 16 / es;
   const bool table16 = d.rotary_dim == 0 || aligned_to(cos_sin, 16);

@@ -1,6 +1,7 @@
 // Appends and read-backs of so many rows that they are taken in parts, on the CPU: the
 // launches replaced by checks of what they are handed, the pointers that a call need not
-// have NULL.  Built with the sanitizers by the test.
+// have NULL; and queries turned in place, or to rows that overlap them.  Built with the
+// sanitizers by the test.
 #include <stdio.h>
 #include <stdlib.h>
 
@@ -9,6 +10,7 @@
 namespace {
 
 int64_t g_rows, g_launches;
+bool g_any;      // pointers are not checked
 
 [[noreturn]] void die(const char* what, long long a, long long b) {
   printf("%s (%lld, %lld)\n", what, a, b);
@@ -17,6 +19,7 @@ int64_t g_rows, g_launches;
 }
 
 void take(const void* p, bool there, int64_t row_bytes, const char* what) {
+  if (g_any) return;
   const int64_t want = there ? (int64_t{1} << 44) + g_rows * row_bytes : 0;
   if (reinterpret_cast<int64_t>(p) != want) die(what, reinterpret_cast<int64_t>(p), want);
 }
@@ -34,7 +37,7 @@ void rows(int64_t T, const int32_t* positions, const int64_t* slots) {
 
 namespace sv {
 int32_t record_error(int32_t code, const char* msg) noexcept {
-  printf("%s\n", msg);
+  if (!msg[0]) die("no message", code, 0);
   return code;
 }
 hipError_t launch_rotary(const RotaryArgs& a, int, bool, hipStream_t) {
@@ -98,6 +101,26 @@ int main() {
               s = kv_cache_read_q4(T, kv, dim, 16, nb, SV_DTYPE_BF16, L, pages, pages, pages, scales, P, P, nullptr);
               if (s != SV_OK || g_rows != T) die("read", s, g_rows);
             }
+  // Queries of 2 heads of 64 (256 bytes a row) to rows `by` bytes on.
+  struct Place { int32_t T; int64_t stride, out_stride, by; bool fine; };
+  const Place places[] = {
+      {5, 0, 0, 0, true}, {5, 512, 512, 0, true}, {5, 512, 0, 0, false}, {5, 0, 512, 0, false},
+      {1, 512, 0, 0, true}, {1, 0, 0, 128, false}, {1, 0, 0, 256, true}, {1, 0, 0, -254, false},
+      {5, 0, 0, 256, false}, {5, 0, 0, 1024, false}, {5, 0, 0, 1278, false}, {5, 0, 0, 1280, true},
+      {5, 0, 0, -1278, false}, {5, 0, 0, -1280, true}, {5, 512, 512, 512, true}, {5, 512, 512, 510, true},
+      {5, 512, 512, 768, true}, {5, 512, 512, 770, false}, {5, 512, 512, 1024, false},
+      {5, 512, 512, -512, true}, {5, 512, 512, -2046, false}, {5, 512, 512, 5118, true}, {5, 512, 1024, 512, true}};
+  g_any = true;
+  for (const Place& at : places)
+    for (bool q4 : {false, true}) {
+      spec_kv_rotary_desc d{};
+      d.tokens = at.T, d.heads = 2, d.kv_heads = 1, d.head_dim = 64, d.block_size = 16, d.num_blocks = 9;
+      d.dtype = SV_DTYPE_BF16, d.rotary_dim = 64, d.table_rows = 9;
+      d.q_stride = at.stride, d.q_out_stride = at.out_stride;
+      const int32_t s = q4 ? kv_cache_append_q4(&d, P, P, P, I, F, L, P + at.by, P, P, P, F, nullptr)
+                           : kv_cache_append_rotary(&d, P, P, P, I, F, L, P + at.by, P, P, nullptr);
+      if (s != (at.fine ? SV_OK : SV_ERR_INVALID_ARG)) die("in place", s, at.by);
+    }
   printf("parts ok: %ld launches of the 4-bit append\n", parts);
   return parts > 200 ? 0 : 1;
 }
