@@ -291,9 +291,12 @@ size_t kv_paged_attention_q4_workspace_bytes(const spec_kv_attention_desc* desc)
  * per 32.  A query's pieces add up to it: channels of a 128th of the largest of their
  * 32 (f16: of a 512th) are held whole, smaller ones within 2^-14 of the largest (f16:
  * 2^-19).  A softmax weight times its value's scale: within 2^-14 of the largest of 32
- * positions (2^-104 at least, where the row's largest weight is 2^-8).  A query row with an
- * infinity or NaN gets NaN in out and lse if it sees a position, and so does a row
- * that sees a key or value that is not a finite number, or whose scores leave float32.
+ * positions (2^-104 at least, where the row's largest weight is 2^-8).
+ * A query row with an infinity or NaN gets NaN in out and lse if it sees a position, and
+ * so does a row that sees a key that is not a number, or whose product with a key leaves
+ * float32 upwards (or has parts beyond it of both signs).  One that leaves it
+ * downwards has no weight, as a score of -inf.  A value that is not finite makes
+ * the row's out NaN and leaves its lse.
  * What lies at positions that a row does not see never reaches it, whatever it is. */
 int32_t kv_paged_attention_q4(const spec_kv_attention_desc* desc, const void* q,
                               const void* k_codes, const void* k_scales, const void* v_codes,

@@ -511,7 +511,8 @@ def kv_paged_attention_q4(q, cache, block_table, seq_lens, cu_tokens, *, scale=N
                           sliding_window=0, max_new=0, lse=False, out=None, workspace=None):
     """``kv_paged_attention`` over a 4-bit ``cache``: ``q`` [T, heads, head_dim] bfloat16
     or float16, head_dim a multiple of 32 up to 256, everything else as there.  A query
-    row that holds an infinity or NaN gives NaN."""
+    row that holds an infinity or NaN gives NaN; a value row that does makes ``out`` NaN
+    where it is seen, and leaves ``lse``."""
     lib = _pkg.library()
     desc, pointers = _attention_q4_desc(q, cache, block_table, scale, sliding_window, max_new)
     return _attend(lib.kv_paged_attention_q4, lib.kv_paged_attention_q4_workspace_bytes, desc, q,
