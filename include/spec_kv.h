@@ -46,6 +46,9 @@
 extern "C" {
 #endif
 
+/* Raised where a call or a struct of this header changes.  Calls that are added
+ * leave it (the rotated append and the 4-bit cache came after the first ones): a
+ * program that finds the library at run time asks for their symbols. */
 #define SPEC_KV_ABI_VERSION 1
 
 #define SV_DTYPE_F16 2        /* float16, caches and attention only              */
