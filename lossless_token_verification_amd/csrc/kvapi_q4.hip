@@ -149,18 +149,18 @@ int32_t check_q4_cache(bool any, const void* k_codes, const void* k_scales, cons
 // The kernel for an attention call over 4-bit pages: tiles of 16 rows a wavefront, with
 // as many wavefronts as the rows of one sequence and key head need, 4 where they are
 // more.  64 sequences of 2000 positions, head_dim 128, in tiles of 16 / 32 / 48 / 64 rows:
-//   12 rows each  45 / 44 / 48 / 48 us     24  56 / 44 / 47 / 48     36  89 / 57 / 48 / 50
-//   60            96 / 57 / 83 / 49        prompts of 2500 tokens (4)  524 / 278 / 249 / 234
-// (single tokens, 16 against 32 rows: 142 and 155 us for 256 sequences of 2300 positions,
-// head_dim 64: 75 and 100; head_dim 256 has no tile of 16, whose wavefront would spill:
-// 572 us against 75 for 64 sequences of 2300).  Tiles of 96 and 128 rows took 633 and
-// 490 us where 64 took 423.
+//   12 rows each  45 / 51 / 54 / 55 us     24  60 / 49 / 54 / 54     36  97 / 65 / 55 / 55
+//   60           106 / 63 / 92 / 54        prompts of 2500 tokens (4)  573 / 310 / 281 / 264
+// (head_dim 64, 12 rows: 35 / 45 / 46 / 48; head_dim 256 has no tile of 16, whose wavefront
+// would spill: 596 us against 79 for single tokens of 64 sequences of 2300.  Tiles of 96 and
+// 128 rows were slower than 64 in an earlier form of the kernel, 633 and 490 us against
+// 423.)
 // The keys are split until about `wgs` workgroups have work.  One wavefront each: 4
-// sequences of 100000 at head_dim 64 and 128 take 85 and 103 us with 512, 68 and 97 with 1024,
-// 61 and 107 with 2048.  More wavefronts: 64 sequences of 2300, 9 tokens each, 46 and 58 us with
-// 512, 58 and 72 with 1024 (more to join); one sequence of 30000, 40 tokens, 37 and 44 us with
-// 512, 43 and 53 with 256.  A split may be a single unit: one token over 1000 positions takes
-// 12.1 us, 14.3 with two at least.
+// sequences of 100000 at head_dim 64 and 128 take 94 and 105 us with 512, 70 and 89 with 1024,
+// 56 and 99 with 2048.  More wavefronts: 64 sequences of 2300, 9 tokens each, 49 and 59 us with
+// 512, 61 and 76 with 1024 (more to join); one sequence of 30000, 40 tokens, 38 and 46 us with
+// 512, 46 and 55 with 256.  A split may be a single unit: one token over 1000 positions takes
+// 12.4 us, 14.8 with two at least.
 sv::AttendShape q4_shape(const spec_kv_attention_desc& d) {
   sv::AttendShape s{};
   const int64_t mean = d.batch > 0 ? (static_cast<int64_t>(d.tokens) + d.batch - 1) / d.batch : 1;

@@ -31,17 +31,18 @@
 //
 // A wavefront takes 16 query rows (of the tokens of one sequence and the heads that
 // share a key head), a workgroup 1 to 4 of them, so that one load of a unit of 128
-// positions (8.75 KB of keys, as much of values, at head_dim 128) serves them all.  Two
-// units lie in LDS, loaded directly.  The split of a weight (32 conversions and their
-// remainders, some 400 instructions a unit) is what no row shares with another.
-// What bounds it, bfloat16, 32 query and 8 key heads of 128:
-//   256 sequences of 512 to 4096 positions, 9 tokens each (719 MB): 160 us, 4.5 TB/s; with
-//     the arithmetic left out the loads take 150 (a short sequence fills its buffers
-//     anew), and the arithmetic of three wavefronts is as long as they are;
-//   4 sequences of 125000, single tokens (553 MB): 98 us, 5.6 TB/s, the loads;
-//   4 prompts of 2200 to 3800 tokens (332 GFLOP): 350 to 390 us; the vector instructions
-//     of softmax and splits (60 % of the cycles), then the matrix instructions (a
-//     quarter), not the loads (150 to 186).
+// positions (8704 bytes of keys, as many of values, at head_dim 128) serves them all.  Two
+// units lie in LDS, loaded directly.  The weights and their split (some 370 vector
+// instructions a unit for 16 rows) are what no row shares with another.
+// What bounds it, bfloat16, 32 query and 8 key heads of 128 (shares of the cycles by
+// the counters; loads: with the arithmetic left out):
+//   256 sequences of 512 to 4096 positions, 9 tokens each (719 MB): 185 us, 3.9 TB/s; the
+//     loads take 137 (a short sequence fills its buffers anew), vector instructions are
+//     issued in 56 % of the cycles, the matrix cores busy in 19 %;
+//   4 sequences of 125000, single tokens (553 MB): 106 us, 5.2 TB/s, the loads (102);
+//   4 prompts of 2200 to 3800 tokens (332 GFLOP): 395 us; the vector instructions of
+//     softmax and splits (74 % of the cycles), then the matrix cores (24 %), not the
+//     loads (138).
 #pragma once
 
 #include "kvattend_mfma.h"
@@ -139,15 +140,18 @@ struct Q4Cfg {
   static constexpr int IDS = (CHUNKS * RPL + kWave - 1) / kWave;   // its lookups, per unit
   static constexpr int OT = D / 16;                        // result tiles
   // Sequences of a thread that the work search holds in registers: 256 single tokens over
-  // 100 positions take 25.8 us, 27.8 without; over 2300 142 and 147.
+  // 100 positions take 26.0 us, 28.3 without; over 2300 133 and 138.
   static constexpr int kHeld = W < 3 ? 4 : 2;
   // Nontemporal loads where a sequence's keys are mostly read by one tile: 256 sequences of
-  // 2300 positions, single tokens 142 against 154 us, 9 tokens 188 against 195; with more
-  // tiles (prompts) the two measure the same, and the next tile finds keys in the cache.
+  // 2300 positions, single tokens 133 against 142 us, 9 tokens 189 against 194; with more
+  // tiles the next one finds keys in the cache (prompts of 2500 270 against 264).
   static constexpr bool kOnce = MT <= 48;
   // Wavefronts to a SIMD, by the registers.  Three, although some values then lie in
-  // scratch memory (float16 at head_dim 128, 3 or 4 wavefronts): 256 sequences of 2300, 9
-  // tokens, 213 us against 232 with two, prompts of 2500 294 against 315.
+  // scratch memory (12 to 40 bytes a lane): 256 sequences of 2300, 9 tokens, head_dim 128
+  // bfloat16 190 us against 218 with two, float16 197 against 231, head_dim 64 (512 to
+  // 4096 positions) 140 against 185; prompts of 2500 264 and 307, 278 and 317, 222 and 268.
+  // Two where three spill in the loop: head_dim 256, prompts 455 against 706 (up to 64
+  // bytes with two), or have no more to hide: one wavefront of head_dim 64 73 against 83.
   static constexpr int kPerSimd = D == 256 || W == 1 || (D == 128 && W == 2) ? 2 : 3;
 };
 
