@@ -258,7 +258,7 @@ int32_t kv_cache_append_rotary(const spec_kv_rotary_desc* desc, const void* q, c
  *   k_scales          [.., 4 ceil(head_dim / 128)] bytes: byte g is b for channels
  *                     32 g .. 32 g + 31, whose unit is 2^(b - 127); 255: not a
  *                     number.  Bytes behind head_dim / 32 are not used;
- *   v_scales          [..] float32: the unit of a whole row, not negative.
+ *   v_scales          [..] float32: the unit of a whole row, its sign bit 0.
  * The append picks the least 2^e with amax <= 7 * 2^e for the channels of a key
  * (no less than 2^-127), amax / 6 rounded to 8 significant bits (float32, then to
  * bfloat16's precision) for a value row, and for each channel the level nearest to
@@ -293,8 +293,9 @@ size_t kv_paged_attention_q4_workspace_bytes(const spec_kv_attention_desc* desc)
  * against the codes is split into pieces of 4 significant bits with a power of two
  * per 32.  A query's pieces add up to it: channels of a 128th of the largest of their
  * 32 (f16: of a 512th) are held whole, smaller ones within 2^-14 of the largest (f16:
- * 2^-19).  A softmax weight times its value's scale: within 2^-14 of the largest of 32
- * positions (2^-104 at least, where the row's largest weight is 2^-8).
+ * 2^-19; the largest counts as 2^-102 at least).  A softmax weight times its value's
+ * scale: within 2^-14 of the largest of 32 positions (2^-103 at least, where the row's
+ * largest weight is 2^-8).
  * A query row with an infinity or NaN gets NaN in out and lse if it sees a position, and
  * so does a row that sees a key that is not a number, or whose product with a key leaves
  * float32 upwards (or has parts beyond it of both signs).  One that leaves it

@@ -87,7 +87,7 @@ __device__ __forceinline__ f32x32 from_fp6(u32x6 x, float s) {
 }
 
 // The N pieces of 32 numbers, even ones in x0 and odd ones in x1, the largest of
-// magnitude `top` (as bits), scaled so that it is in [2, 4).  Numbers below 2^-104 lose bits (the first piece's scale is 2^-103 at least, so that the
+// magnitude `top` (as bits), scaled so that it is in [2, 4).  Numbers below 2^-102 lose bits (the first piece's scale is 2^-103 at least, so that the
 // last one's is a number).
 template <int N>
 __device__ __forceinline__ void split_pieces(f32x16 x0, f32x16 x1, uint32_t top, u32x6 (&piece)[N],
