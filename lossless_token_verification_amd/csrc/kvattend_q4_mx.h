@@ -87,8 +87,8 @@ __device__ __forceinline__ f32x32 from_fp6(u32x6 x, float s) {
 }
 
 // The N pieces of 32 numbers, even ones in x0 and odd ones in x1, the largest of
-// magnitude `top` (as bits), scaled so that it is in [2, 4).  Numbers below 2^-102 lose bits (the first piece's scale is 2^-103 at least, so that the
-// last one's is a number).
+// magnitude `top` (as bits), scaled so that it is in [2, 4).  Numbers below 2^-102 lose
+// bits (the first piece's scale is 2^-103 at least, so that the last one's is a number).
 template <int N>
 __device__ __forceinline__ void split_pieces(f32x16 x0, f32x16 x1, uint32_t top, u32x6 (&piece)[N],
                                              int (&scale)[N]) {
@@ -194,7 +194,7 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
     const int pos = it.pos0 + q_token - it.token0;
     const int key_last = min(pos, it.key_hi - 1);
     const int key_first = a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
-    see_lo = key_last >= key_first ? key_first : INT32_MAX;
+    see_lo = key_last >= key_first ? key_first : INT32_MIN;
     see_span = key_last >= key_first ? key_last - key_first : 0;
   }
   // positions every row of the tile may see: units inside need no mask
@@ -214,17 +214,18 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
   const int wave_row = wave * (CHUNKS * RPL);
   auto in_unit = [&](int i) { return wave_row + i * kWave + lane; };   // (may be past the unit)
   auto own_row = [&](int i) { return i * kWave + lane < CHUNKS * RPL && in_unit(i) < KT; };
-  auto nearest = [&](int key) { return min(max(key, it.key_lo), it.key_hi - 1); };
+  // (past 2^31 - 1, behind the last unit of the longest sequences, that is key_lo)
+  auto nearest = [&](uint32_t key) { return min(max(static_cast<int>(key), it.key_lo), it.key_hi - 1); };
   auto paged = [&](int id) { return id >= 0 && id < a.num_blocks; };
   int32_t* const ids = sid + wave * (2 * IDS * kWave);
-  auto look = [&](int slot, int base) {     // starts the lookups of the unit at position `base`
+  auto look = [&](int slot, uint32_t base) {     // starts the lookups of the unit at position `base`
 #pragma unroll
     for (int i = 0; i < IDS; ++i)
       __builtin_amdgcn_global_load_lds((gptr_t)(table + fast_div(nearest(base + in_unit(i)), a.bs)),
                                        (lptr_t)(ids + (slot * IDS + i) * kWave), 4, 0, 0);
   };
   uint32_t off[IDS];
-  auto turn = [&](int slot, int n, int base) {   // the n-th unit, looked up, is the next to load
+  auto turn = [&](int slot, int n, uint32_t base) {   // the n-th unit, looked up, is the next to load
 #pragma unroll
     for (int i = 0; i < IDS; ++i) {
       const int id = ids[(slot * IDS + i) * kWave + lane];
@@ -239,8 +240,9 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
   // through scalar registers.
   const int lq = lane / NV, lslot = lane & (NV - 1);
   const bool whole_rows = a.block_size % RPL == 0;
-  auto load_unit = [&](int base, char* sb) {
-    const bool inside = whole_rows && base >= it.key_lo && base + KT <= it.key_hi;
+  auto load_unit = [&](uint32_t from_key, char* sb) {
+    const int base = static_cast<int>(from_key);
+    const bool inside = whole_rows && base >= it.key_lo && base <= it.key_hi - KT;
 #pragma unroll
     for (int i = 0; i < CHUNKS; ++i) {
       const int j = wave * CHUNKS + i;               // which RPL rows
@@ -298,10 +300,10 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
     }
   }
   const int n_units = it.u1 - it.u0;
-  const int first = it.u0 * KT;
+  auto unit_key = [&](int n) { return static_cast<uint32_t>(it.u0 + n) * KT; };   // of the n-th unit
   if (n_units > 0) {
-    look(0, first);
-    look(1, first + KT);
+    look(0, unit_key(0));
+    look(1, unit_key(1));
     if (C::kPad) {
       // (vectors that a row does not have are loaded by no one: zero from here on)
       for (int i = tid; i < C::kKS / 16; i += C::W * kWave) {
@@ -312,11 +314,11 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
     if (tid < 8) missing[tid] = 0;
     wait_loads();
     __syncthreads();
-    turn(0, 0, first);
-    load_unit(first, sb0);
-    turn(1, 1, first + KT);
+    turn(0, 0, unit_key(0));
+    load_unit(unit_key(0), sb0);
+    turn(1, 1, unit_key(1));
     wait_entries();
-    look(0, first + 2 * KT);
+    look(0, unit_key(2));
   }
   u32x6 qf[HALVES][QS];
   int qs[HALVES];        // a byte for each step's pieces
@@ -410,13 +412,13 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
     }
     if (!masked) return;
     // a row that sees nothing has span 0 at a position that is none
-    const int d = u * KT + 4 * g - see_lo;
+    const uint32_t d = static_cast<uint32_t>(u * KT + 4 * g) - static_cast<uint32_t>(see_lo);
     dead = 0;
 #pragma unroll
     for (int t = 0; t < 8; ++t)
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        dead |= (static_cast<uint32_t>(d + t * 16 + r) > see_span ? 1u : 0u) << (4 * t + r);
+        dead |= (d + t * 16 + r > see_span ? 1u : 0u) << (4 * t + r);
     if (missing[n & 7] == n + 1) {
       const int b0 = u * KT + lane;
       const uint64_t page0 = __ballot(paged(table[fast_div(nearest(b0), a.bs)]));
@@ -530,9 +532,9 @@ attend_q4_kernel(AttendArgs a, Q4Cache cache) {
     auto step = [&](auto kFirst, int n, int slot, char* now, char* next) {
       wait_loads();
       __builtin_amdgcn_s_barrier();
-      load_unit(first + (n + 1) * KT, next);
-      turn(slot, n + 2, first + (n + 2) * KT);
-      look(1 - slot, first + (n + 3) * KT);
+      load_unit(unit_key(n + 1), next);
+      turn(slot, n + 2, unit_key(n + 2));
+      look(1 - slot, unit_key(n + 3));
       if (n < n_units) compute(kFirst, now, it.u0 + n, n);
     };
     step(std::true_type{}, 0, 0, sb0, sb1);
