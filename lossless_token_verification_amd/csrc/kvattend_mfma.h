@@ -231,7 +231,7 @@ attend_mfma_kernel(AttendArgs a) {
     const int pos = it.pos0 + token - it.token0;
     const int key_last = min(pos, it.key_hi - 1);
     const int key_first = a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
-    see_lo = key_last >= key_first ? key_first : INT32_MAX;
+    see_lo = key_last >= key_first ? key_first : INT32_MIN;
     see_span = key_last >= key_first ? key_last - key_first : 0;
     const T* qr = static_cast<const T*>(a.q) + token * a.q_stride + static_cast<int64_t>(head) * dim;
 #pragma unroll
@@ -250,10 +250,13 @@ attend_mfma_kernel(AttendArgs a) {
   const int64_t head_off = static_cast<int64_t>(h) * a.block_size;
   // Lane l looks up position base + l: its element offset in the caches, and
   // whether there is such a page.  Positions outside the item's range read the
-  // nearest one inside (and are masked); a missing page reads block 0.
-  auto nearest = [&](int base) { return min(max(base + lane, it.key_lo), it.key_hi - 1); };
-  auto entry = [&](int base) { return table + fast_div(nearest(base), a.bs); };
-  auto offset = [&](int base, int id) -> int64_t {
+  // nearest one inside (and are masked; past 2^31 - 1, behind the last unit of the longest
+  // sequences, that is key_lo); a missing page reads block 0.
+  auto nearest = [&](uint32_t base) {
+    return min(max(static_cast<int>(base + lane), it.key_lo), it.key_hi - 1);
+  };
+  auto entry = [&](uint32_t base) { return table + fast_div(nearest(base), a.bs); };
+  auto offset = [&](uint32_t base, int id) -> int64_t {
     const int key = nearest(base);
     const int r = key - fast_div(key, a.bs) * a.block_size;
     const int safe = id >= 0 && id < a.num_blocks ? id : 0;
@@ -272,14 +275,15 @@ attend_mfma_kernel(AttendArgs a) {
   // moves through scalar registers; otherwise every lane fetches its row's.  Lanes
   // of vectors that a row does not have (kPad) load nothing: those places of a
   // buffer are the same in every unit and hold the zeros they started with.
-  auto load_unit = [&](int base, int64_t off, int from, uint16_t* sb) {
+  auto load_unit = [&](uint32_t from_key, int64_t off, int from, uint16_t* sb) {
+    const int base = static_cast<int>(from_key);
     constexpr int kUnroll = C::LOADS > (C::kPad ? 4 : 8) ? 4 : C::LOADS;
     int lk = lslot ^ swz_k<D>(lq), lv = lslot ^ swz_v<D>(lq);
     if (D != 128 || C::LOADS > 4) {   // registers are short: formed at each load
       lk = fresh(lk);
       lv = fresh(lv);
     }
-    if (whole_rows && base >= it.key_lo && base + KT <= it.key_hi) {
+    if (whole_rows && base >= it.key_lo && base <= it.key_hi - KT) {
       const int lo = static_cast<int>(off), hi = static_cast<int>(off >> 32);
       const uint32_t lane_row = lq * dim * 2;
 #pragma unroll kUnroll
@@ -364,12 +368,12 @@ attend_mfma_kernel(AttendArgs a) {
     if (decltype(always_mask)::value || u * KT + KT - 1 > all_hi || u * KT < all_lo) {
       // key_lo <= position <= key_hi as one unsigned comparison; a row that sees
       // nothing has span 0 at a position that is none
-      const int d = u * KT + 4 * hi_lane - see_lo;
+      const uint32_t d = static_cast<uint32_t>(u * KT + 4 * hi_lane) - static_cast<uint32_t>(see_lo);
 #pragma unroll
       for (int t = 0; t < ST; ++t)
 #pragma unroll
         for (int r = 0; r < SR; ++r)
-          st[t][r] = static_cast<uint32_t>(d + at(t, r)) > see_span ? -INFINITY : st[t][r];
+          st[t][r] = d + at(t, r) > see_span ? -INFINITY : st[t][r];
     }
     if (pages != kEvery) {
       const uint64_t here = pages >> (4 * hi_lane);
@@ -461,7 +465,8 @@ attend_mfma_kernel(AttendArgs a) {
         for (int r = 0; r < SR; ++r) zero[r] = 0.0f;
         const acc_t add = mma(one, pf[s], zero);
         const int in = s * kVSpan + k;
-        if (static_cast<uint32_t>(u * KT + in - see_lo) <= see_span && ((pages >> in) & 1)) {
+        const uint32_t d = static_cast<uint32_t>(u * KT + in) - static_cast<uint32_t>(see_lo);
+        if (d <= see_span && ((pages >> in) & 1)) {
 #pragma unroll
           for (int r = 0; r < SR; ++r) x[r] += add[r];
         }
@@ -537,14 +542,14 @@ attend_mfma_kernel(AttendArgs a) {
       __syncthreads();
     }
     uint16_t* const ring[NB] = {sb0, sb1};
-    const int first = it.u0 * KT;
+    const uint32_t first = static_cast<uint32_t>(it.u0) * KT;
     int32_t* const ids = sid + wave * C::SUPER;
     int64_t off[IDS];
     uint64_t mask[IDS], mask_next[IDS];
     auto look = [&](int q) {          // starts the lookups of turn q
 #pragma unroll
       for (int i = 0; i < IDS; ++i)
-        __builtin_amdgcn_global_load_lds((gptr_t)entry(first + q * C::SUPER + i * kWave),
+        __builtin_amdgcn_global_load_lds((gptr_t)entry(first + static_cast<uint32_t>(q) * C::SUPER + i * kWave),
                                          (lptr_t)(ids + i * kWave), 4, 0, 0);
     };
     auto turn = [&](int q) {          // turn q, looked up, becomes the one that loads
@@ -552,11 +557,11 @@ attend_mfma_kernel(AttendArgs a) {
       for (int i = 0; i < IDS; ++i) {
         const int id = ids[i * kWave + lane];
         mask_next[i] = paged(id);
-        off[i] = offset(first + q * C::SUPER + i * kWave, id);
+        off[i] = offset(first + static_cast<uint32_t>(q) * C::SUPER + i * kWave, id);
       }
     };
     auto load = [&](int n, int s) {   // unit n = unit s of the turn that loads
-      load_unit(first + n * KT, off[s * KT / kWave], s * KT % kWave, ring[s]);
+      load_unit(first + static_cast<uint32_t>(n) * KT, off[s * KT / kWave], s * KT % kWave, ring[s]);
     };
     look(0);
     wait_loads();
