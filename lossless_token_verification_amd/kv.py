@@ -391,9 +391,9 @@ def kv_cache_append_rotary(q, k, v, positions, cos_sin, slot_map, k_cache, v_cac
     [positions, rotary_dim] float32: the cosines of its angles, then their sines.
     Channel i turns with i + rotary_dim / 2, or, ``interleaved``, 2i with 2i + 1;
     channels behind rotary_dim stay as they are.  Returns the turned queries: ``out``
-    (which may be ``q`` itself, and overlaps it in no other way), or a new tensor.  Rows whose position is not in the
-    table are skipped (their queries left as they were in ``out``), rows without a slot
-    turn their query alone."""
+    (which may be ``q`` itself, and overlaps it in no other way), or a new tensor.  Rows
+    whose position is not in the table are skipped (their queries left as they were in
+    ``out``), rows without a slot turn their query alone."""
     lib = _pkg.library()
     dev = _gpu(k)
     nb, kv, bs, dim, block_stride = _caches(k_cache, v_cache, k.dtype, dev)

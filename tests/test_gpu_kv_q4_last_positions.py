@@ -76,7 +76,7 @@ def test_rows_behind_a_table_that_ends_there(sv, dim, dtype):
     assert sees.sum() == 22
     assert (out.cpu()[~sees] == 0).all() and torch.isneginf(lse.cpu()[~sees]).all()
     assert torch.isfinite(lse.cpu()[sees]).all()
-    # rows that see some, against the same rows of a table with a page more before its end
+    # (and two pages of the table earlier)
     small = _run(sv, q, cache, table[:, :398], [cap + 27 - 2 * bs], [0, new], window, max_new=new)
     ref = Q.reference(dict(q=q.cpu(), cache={n: t[:, :, -64:].cpu() for n, t in cache.items()},
                            block_table=torch.tensor([[1]], dtype=torch.int32),
